@@ -256,7 +256,7 @@ moe_status moe_layer_forward_static(const moe_config* cfg, const float* logits, 
                                     float* topk_w, int32_t* counts, float* balancedness,
                                     void* stream);
 
-/* Where moe_layer_forward (and its _fp8w and _w8a8 forms) leave the
+/* Where moe_layer_forward (and its _fp8w, _w8a8, _mxfp4w and _w4a4 forms) leave the
  * permutation they built inside their workspace, as byte offsets from its
  * start: offsets[0] seg_offsets [S+1], offsets[1] seg_expert [S],
  * offsets[2] assign_to_row [T*k], offsets[3] row_to_token [R] (int32, the
@@ -357,6 +357,118 @@ moe_status moe_layer_forward_w8a8(const moe_config* cfg, const float* logits, co
                                   void* out, int32_t* topk_ids, float* topk_w, int32_t* counts,
                                   float* balancedness, void* workspace, size_t workspace_bytes,
                                   void* stream);
+
+/* ------------------------------------------------------------------------
+ * Routing with a selection bias.  What is selected on and what weighs the
+ * outputs differ: a bias per expert, moved between steps to even the load,
+ * decides who is picked, and the weights come from the scores alone.
+ * ------------------------------------------------------------------------ */
+
+/* moe_route_topk with a selection bias.  Per token, with l its logits:
+ *   s_e = sigmoid(l_e), or (cfg->score softmax) softmax of l over the
+ *         unmasked experts;
+ *   c_e = s_e + bias_e;
+ *   with n_group > 1 (either score) a group's score is the sum of its best
+ *   group_score_topn c (of fewer if fewer are unmasked) and the topk_group
+ *   best groups are kept, the lower group id first on a tie;
+ *   the k largest c of the kept groups win, in descending order, the lower id
+ *   first on a tie;
+ *   w_j = routed_scale * s_j, or routed_scale * s_j / (sum of the winners' s)
+ *   with renormalize = 1 (0 where that sum is 0).
+ * Scores, sums and comparisons are fp64; weights are rounded once to fp32.
+ * An expert is masked for a token if its logit is NaN, -inf or the lowest
+ * finite fp32, and for every token if its bias is NaN or -inf.  A masked
+ * expert is never picked: a slot that finds no expert left gets id -1 and
+ * weight 0 (moe_permute drops it, and a token with no expert gets output 0).
+ * A +inf logit counts as the largest finite fp32.
+ *   logits [T, E] fp32; bias [E] fp32, or NULL for none; routed_scale a host
+ *   value, finite and > 0 (MOE_ERR_INVALID_ARG otherwise);
+ *   topk_ids [T, k] out, topk_w [T, k] out.
+ * Expert groups with softmax scores are valid here and in the calls that do
+ * not route (moe_permute, moe_grouped_ffn*, moe_unpermute_combine, the size
+ * queries) and in the MXFP4 layers below; the other routing calls return
+ * MOE_ERR_UNSUPPORTED for them. */
+moe_status moe_route_biased(const moe_config* cfg, const float* logits, const float* bias,
+                            float routed_scale, int32_t* topk_ids, float* topk_w,
+                            void* stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MXFP4, OCP Microscaling formats).  A
+ * matrix X [R, C] (C a multiple of 32) is held as
+ *   q     [R, C/2] uint8: E2M1 codes (sign, 2 exponent bits, 1 mantissa bit:
+ *         0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), element 2i of a
+ *         row in the low half of byte i, element 2i + 1 in the high half;
+ *   scale [R, C/32] uint8 E8M0: byte b stands for 2^(b - 127), 255 for NaN;
+ *   X[r][c] = E2M1(q) * 2^(scale[r][c/32] - 127).
+ * ------------------------------------------------------------------------ */
+
+/* Quantize rows of fp32 or bf16 (dtype: moe_dtype) to MXFP4: per block of 32
+ * consecutive elements s is the smallest integer in [-127, 127] with
+ * max|block| <= 6 * 2^s (0 for an all-zero block) and a code is the E2M1
+ * value nearest to x / 2^s, ties to even, sign kept.  A block that holds an
+ * infinity or a NaN gets scale 255 and zero codes.  Weights [n, rows, cols]
+ * are n * rows rows.
+ *   src [rows, cols] 16-byte aligned; q [rows, cols/2] out, 16-byte aligned;
+ *   scale [rows, cols/32] out, 4-byte aligned.
+ * MOE_ERR_INVALID_ARG for bad sizes, types or pointers, MOE_ERR_UNSUPPORTED
+ * beyond 2^40 elements; rows == 0 is MOE_OK; asynchronous on `stream`. */
+moe_status moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t cols, const void* src,
+                              uint8_t* q, uint8_t* scale, void* stream);
+
+/* The way back: dst [rows, cols] fp32 or bf16 = the values of q and scale,
+ * exactly (every value of the format but those beyond the largest finite of
+ * dst, which become infinities, is one of dst's); a block with scale 255
+ * becomes NaN.  Sizes, alignment and errors as moe_quantize_mxfp4. */
+moe_status moe_dequantize_mxfp4(int32_t dtype, int64_t rows, int32_t cols, const uint8_t* q,
+                                const uint8_t* scale, void* dst, void* stream);
+
+/* moe_grouped_ffn with MXFP4 expert weights and bf16 activations: w13_q
+ * [E, 2I, H/2] + w13_scale [E, 2I, H/32]; w2_q [E, H, I/2] + w2_scale
+ * [E, H, I/32].  The weights' values are exact in bf16; h and y_perm are
+ * rounded to bf16 as there.  Needs act_dtype bf16 and H, I, shared_I
+ * multiples of 128 (MOE_ERR_UNSUPPORTED otherwise); q 16-byte and scales
+ * 4-byte aligned.  Other arguments, outputs and errors as moe_grouped_ffn.
+ * A weight block with scale 255 makes the outputs it enters NaN. */
+moe_status moe_grouped_ffn_mxfp4w(const moe_config* cfg, const void* x_perm,
+                                  const int32_t* seg_offsets, const int32_t* seg_expert,
+                                  const uint8_t* w13_q, const uint8_t* w13_scale,
+                                  const uint8_t* w2_q, const uint8_t* w2_scale,
+                                  const float* row_scale, void* y_perm, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* moe_grouped_ffn_mxfp4w with MXFP4 activations: x_perm_q [R, H/2] and
+ * x_perm_scale [R, H/32] (moe_permute's x_perm through moe_quantize_mxfp4).
+ * h is rounded to bf16 and quantized by the same rule before GEMM 2; both
+ * GEMMs multiply E2M1 by E2M1 with fp32 accumulation; y_perm stays bf16. */
+moe_status moe_grouped_ffn_w4a4(const moe_config* cfg, const uint8_t* x_perm_q,
+                                const uint8_t* x_perm_scale, const int32_t* seg_offsets,
+                                const int32_t* seg_expert, const uint8_t* w13_q,
+                                const uint8_t* w13_scale, const uint8_t* w2_q,
+                                const uint8_t* w2_scale, const float* row_scale, void* y_perm,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* The whole layer on MXFP4 weights, routed by moe_route_biased (route_bias
+ * may be NULL): moe_layer_forward's steps with the experts (and the shared
+ * expert: shared_w13_q [2*shared_I, H/2] + shared_w13_scale
+ * [2*shared_I, H/32], shared_w2_q [H, shared_I/2] + shared_w2_scale
+ * [H, shared_I/32], all NULL when shared_I == 0) as in
+ * moe_grouped_ffn_mxfp4w, or, for _w4a4, as in moe_grouped_ffn_w4a4 with x
+ * [T, H] bf16 quantized inside the call (into the workspace) before
+ * dispatch.  Other arguments, outputs and errors as moe_layer_forward. */
+moe_status moe_layer_forward_mxfp4w(
+    const moe_config* cfg, const float* logits, const float* route_bias, float routed_scale,
+    const void* x, const uint8_t* w13_q, const uint8_t* w13_scale, const uint8_t* w2_q,
+    const uint8_t* w2_scale, const uint8_t* shared_w13_q, const uint8_t* shared_w13_scale,
+    const uint8_t* shared_w2_q, const uint8_t* shared_w2_scale, void* out, int32_t* topk_ids,
+    float* topk_w, int32_t* counts, float* balancedness, void* workspace, size_t workspace_bytes,
+    void* stream);
+moe_status moe_layer_forward_w4a4(
+    const moe_config* cfg, const float* logits, const float* route_bias, float routed_scale,
+    const void* x, const uint8_t* w13_q, const uint8_t* w13_scale, const uint8_t* w2_q,
+    const uint8_t* w2_scale, const uint8_t* shared_w13_q, const uint8_t* shared_w13_scale,
+    const uint8_t* shared_w2_q, const uint8_t* shared_w2_scale, void* out, int32_t* topk_ids,
+    float* topk_w, int32_t* counts, float* balancedness, void* workspace, size_t workspace_bytes,
+    void* stream);
 
 #ifdef __cplusplus
 }

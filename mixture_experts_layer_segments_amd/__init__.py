@@ -22,5 +22,7 @@ from ._lib import (  # noqa: F401
     moe_workspace_size, moe_quantize_fp8, moe_grouped_ffn_fp8w, moe_layer_forward_fp8w,
     moe_layer_plan_offsets, moe_num_rows, moe_quantize_act_fp8, moe_grouped_ffn_w8a8,
     moe_layer_forward_w8a8, moe_layer_forward_static, MOE_STATIC_WORKSPACE_BYTES,
+    moe_route_biased, moe_quantize_mxfp4, moe_dequantize_mxfp4, moe_grouped_ffn_mxfp4w,
+    moe_grouped_ffn_w4a4, moe_layer_forward_mxfp4w, moe_layer_forward_w4a4,
     EXPORTED_SYMBOLS,
 )

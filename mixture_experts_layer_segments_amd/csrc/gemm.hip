@@ -1444,6 +1444,7 @@ void launch_mfma_pair(const moe_config& c, const FfnProblem* probs, int n_probs,
 void launch_grouped_ffn(const moe_config& c, const FfnProblem* probs, int n_probs,
                         hipStream_t s) {
   const int H = c.H;
+  if (probs[0].mx) return launch_grouped_ffn_mx(c, probs, n_probs, s);
   if (c.act_dtype == MOE_DT_F32) {
     for (int p = 0; p < n_probs; ++p) {
       const FfnProblem& P = probs[p];

@@ -2,6 +2,7 @@
 // Every check runs on the host before any HIP call, so a bad call returns a
 // status without touching the GPU (and can be tested on a machine without
 // one).
+#include <math.h>
 #include <string.h>
 
 #include <atomic>
@@ -81,7 +82,9 @@ int device_cu_count() {
 
 namespace {
 
-moe_status check_config(const moe_config* c) {
+// (softmax_groups: the caller routes with moe_route_biased's rules, which take
+// expert groups with softmax scores too)
+moe_status check_config(const moe_config* c, bool softmax_groups = false) {
   if (!c) return MOE_ERR_INVALID_ARG;
   if (c->T < 0 || c->H <= 0 || c->E <= 0 || c->k <= 0 || c->I <= 0) return MOE_ERR_INVALID_ARG;
   if (c->E > kMaxE || c->k > kMaxK) return MOE_ERR_UNSUPPORTED;
@@ -92,7 +95,7 @@ moe_status check_config(const moe_config* c) {
   if (c->n_group <= 0 || c->E % c->n_group != 0) return MOE_ERR_INVALID_ARG;
   if (c->n_group > 64) return MOE_ERR_UNSUPPORTED;
   if (c->n_group > 1) {
-    if (c->score != MOE_SCORE_SIGMOID) return MOE_ERR_UNSUPPORTED;
+    if (c->score != MOE_SCORE_SIGMOID && !softmax_groups) return MOE_ERR_UNSUPPORTED;
     const int per = c->E / c->n_group;
     if (c->topk_group <= 0 || c->topk_group > c->n_group) return MOE_ERR_INVALID_ARG;
     if ((int64_t)c->topk_group * per < c->k) return MOE_ERR_INVALID_ARG;
@@ -139,8 +142,8 @@ using namespace moe;
 
 namespace {
 
-// Expert weights of one call: bf16 (scales NULL), or E4M3 codes with 128 x 128
-// block scales.
+// Expert weights of one call: bf16 (scales NULL), E4M3 codes with 128 x 128
+// block scales, or MXFP4 (mx: E2M1 codes with E8M0 scales per 1 x 32).
 struct Weights {
   const void* w13;
   const void* w2;
@@ -148,30 +151,57 @@ struct Weights {
   const float* w2_scale;
   bool fp8;
   bool acts_fp8 = false;   // with fp8: E4M3 activations too (W8A8)
+  bool mx = false;
+  const uint8_t* w13_e8 = nullptr;
+  const uint8_t* w2_e8 = nullptr;
+  bool acts_mx = false;    // with mx: MXFP4 activations too (W4A4)
 };
 
-// Extra requirements of FP8 weights: bf16 activations, 128-multiples, scales.
+Weights mx_weights(const uint8_t* w13, const uint8_t* w13_e8, const uint8_t* w2,
+                   const uint8_t* w2_e8, bool acts) {
+  return Weights{w13, w2, nullptr, nullptr, false, false, true, w13_e8, w2_e8, acts};
+}
+
+// A routing with a selection bias (moe_route_biased) instead of
+// moe_route_topk's.
+struct BiasedRouting {
+  const float* bias;       // nullable
+  float scale;
+};
+bool valid(const BiasedRouting& b) {
+  return isfinite(b.scale) && b.scale > 0.0f && aligned(b.bias, 4);
+}
+
+// Extra requirements of FP8 and MXFP4 weights: bf16 activations,
+// 128-multiples, scales.
 moe_status check_fp8(const moe_config* cfg, const Weights& w) {
-  if (!w.fp8) return MOE_OK;
+  if (!w.fp8 && !w.mx) return MOE_OK;
   if (cfg->act_dtype != MOE_DT_BF16) return MOE_ERR_UNSUPPORTED;
   if (cfg->H % 128 || cfg->I % 128 || cfg->shared_I % 128) return MOE_ERR_UNSUPPORTED;
+  if (w.mx) {
+    if (!w.w13_e8 || !w.w2_e8) return MOE_ERR_INVALID_ARG;
+    if (!aligned(w.w13_e8, 4) || !aligned(w.w2_e8, 4)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+  }
   if (!w.w13_scale || !w.w2_scale) return MOE_ERR_INVALID_ARG;
   if (!aligned(w.w13_scale, 4) || !aligned(w.w2_scale, 4)) return MOE_ERR_INVALID_ARG;
   return MOE_OK;
 }
 
-moe_status grouped_ffn(const moe_config* cfg, const void* x_perm, const float* x_perm_scale,
+// (x_perm_scale: fp32 scales of E4M3 rows or E8M0 bytes of MXFP4 rows, else NULL)
+moe_status grouped_ffn(const moe_config* cfg, const void* x_perm, const void* x_perm_scale,
                        const int32_t* seg_offsets, const int32_t* seg_expert, const Weights& w,
                        const float* row_scale, void* y_perm, void* workspace,
                        size_t workspace_bytes, void* stream) {
-  moe_status st = check_config(cfg);
+  moe_status st = check_config(cfg, true);
   if (st != MOE_OK) return st;
   if (!w.w13 || !w.w2) return MOE_ERR_INVALID_ARG;
   if ((st = check_fp8(cfg, w)) != MOE_OK) return st;
   if (cfg->T == 0) return MOE_OK;
   if (!x_perm || !seg_offsets || !seg_expert || !y_perm || !workspace)
     return MOE_ERR_INVALID_ARG;
-  if (w.acts_fp8 && (!x_perm_scale || !aligned(x_perm_scale, 4))) return MOE_ERR_INVALID_ARG;
+  if ((w.acts_fp8 || w.acts_mx) && (!x_perm_scale || !aligned(x_perm_scale, 4)))
+    return MOE_ERR_INVALID_ARG;
   if (!aligned(x_perm, 16) || !aligned(w.w13, 16) || !aligned(w.w2, 16) ||
       !aligned(y_perm, 16) || !aligned(workspace, kAlign) || !aligned(seg_offsets, 4) ||
       !aligned(seg_expert, 4) || (row_scale && !aligned(row_scale, 4)))
@@ -197,7 +227,13 @@ moe_status grouped_ffn(const moe_config* cfg, const void* x_perm, const float* x
   p.n_w = cfg->E;
   p.Iw = cfg->I;
   p.a_fp8 = w.acts_fp8;
-  p.a_scale = x_perm_scale;
+  p.a_scale = (const float*)x_perm_scale;
+  p.mx = w.mx;
+  p.mx_acts = w.acts_mx;
+  p.w13_e8 = w.w13_e8;
+  p.w2_e8 = w.w2_e8;
+  p.a_e8 = (const uint8_t*)x_perm_scale;
+  p.h_e8 = (uint8_t*)(ws + L.h_s);   // (as many bytes as the 1 x 128 fp32 scales)
   p.h_q = (uint8_t*)(ws + L.h_q);
   p.h_scale = (float*)(ws + L.h_s);
   p.a_deq = ws + L.a_deq;
@@ -209,9 +245,11 @@ moe_status grouped_ffn(const moe_config* cfg, const void* x_perm, const float* x
 moe_status layer_forward(const moe_config* cfg, const float* logits, const void* x,
                          const Weights& w, const Weights& sw, void* out, int32_t* topk_ids,
                          float* topk_w, int32_t* counts, float* balancedness, void* workspace,
-                         size_t workspace_bytes, void* stream) {
-  moe_status st = check_config(cfg);
+                         size_t workspace_bytes, void* stream,
+                         const BiasedRouting* biased = nullptr) {
+  moe_status st = check_config(cfg, biased != nullptr);
   if (st != MOE_OK) return st;
+  if (biased && !valid(*biased)) return MOE_ERR_INVALID_ARG;
   const bool shared = cfg->shared_I > 0;
   if (!w.w13 || !w.w2 || (shared && (!sw.w13 || !sw.w2))) return MOE_ERR_INVALID_ARG;
   if ((st = check_fp8(cfg, w)) != MOE_OK) return st;
@@ -243,8 +281,19 @@ moe_status layer_forward(const moe_config* cfg, const float* logits, const void*
     xa = ws + L.x_q;
     xs = (const float*)(ws + L.x_s);
   }
+  // MXFP4 activations: likewise, in 1 x 32 blocks (half the bytes; as many of
+  // scales)
+  if (w.acts_mx) {
+    launch_quantize_mxfp4(MOE_DT_BF16, (int64_t)cfg->T * cfg->H, x, (uint8_t*)(ws + L.x_q),
+                          (uint8_t*)(ws + L.x_s), s);
+    xa = ws + L.x_q;
+  }
   // no x_perm: GEMM 1 gathers its rows from x through row_to_token
-  if (cfg->T * cfg->k <= kSmallA) {
+  if (biased) {
+    launch_route_biased(*cfg, logits, biased->bias, biased->scale, topk_ids, topk_w, s);
+    launch_permute(*cfg, x, topk_ids, nullptr, seg_offsets, seg_expert, a2r, r2t, counts,
+                   balancedness, topk_w, row_w, ws, L, s);
+  } else if (cfg->T * cfg->k <= kSmallA) {
     launch_route_permute_small(*cfg, logits, topk_ids, topk_w, counts, seg_offsets, seg_expert,
                                a2r, r2t, row_w, balancedness, s);
   } else {
@@ -262,6 +311,12 @@ moe_status layer_forward(const moe_config* cfg, const float* logits, const void*
   p[0].a_deq = ws + L.a_deq;
   p[0].a_deq_bytes = L.g_end - L.a_deq;
   p[0].a_rows = r2t;
+  p[0].mx = w.mx;
+  p[0].mx_acts = w.acts_mx;
+  p[0].w13_e8 = w.w13_e8;
+  p[0].w2_e8 = w.w2_e8;
+  p[0].a_e8 = (const uint8_t*)(ws + L.x_s);
+  p[0].h_e8 = (uint8_t*)(ws + L.h_s);
   p[0].w13 = w.w13;
   p[0].w2 = w.w2;
   p[0].w_fp8 = w.fp8;
@@ -287,6 +342,12 @@ moe_status layer_forward(const moe_config* cfg, const float* logits, const void*
     p[1].h_scale = (float*)(ws + L.shared_hs);
     p[1].a_deq = ws + L.a_deq;
     p[1].a_deq_bytes = L.g_end - L.a_deq;
+    p[1].mx = sw.mx;
+    p[1].mx_acts = sw.acts_mx;
+    p[1].w13_e8 = sw.w13_e8;
+    p[1].w2_e8 = sw.w2_e8;
+    p[1].a_e8 = (const uint8_t*)(ws + L.x_s);
+    p[1].h_e8 = (uint8_t*)(ws + L.shared_hs);
     p[1].w13 = sw.w13;
     p[1].w2 = sw.w2;
     p[1].w_fp8 = sw.fp8;
@@ -376,22 +437,22 @@ const char* moe_status_string(moe_status s) {
 }
 
 int32_t moe_num_segments(const moe_config* cfg) {
-  if (check_config(cfg) != MOE_OK) return -1;
+  if (check_config(cfg, true) != MOE_OK) return -1;
   return num_segments(*cfg);
 }
 
 int32_t moe_num_rows(const moe_config* cfg) {
-  if (check_config(cfg) != MOE_OK) return -1;
+  if (check_config(cfg, true) != MOE_OK) return -1;
   return (int32_t)num_rows(*cfg);
 }
 
 size_t moe_workspace_size(const moe_config* cfg) {
-  if (check_config(cfg) != MOE_OK) return 0;
+  if (check_config(cfg, true) != MOE_OK) return 0;
   return make_layout(*cfg).l_end;
 }
 
 moe_status moe_layer_plan_offsets(const moe_config* cfg, size_t offsets[4]) {
-  const moe_status st = check_config(cfg);
+  const moe_status st = check_config(cfg, true);
   if (st != MOE_OK) return st;
   if (!offsets) return MOE_ERR_INVALID_ARG;
   const Layout L = make_layout(*cfg);
@@ -414,12 +475,26 @@ moe_status moe_route_topk(const moe_config* cfg, const float* logits, int32_t* t
   return launch_status();
 }
 
+moe_status moe_route_biased(const moe_config* cfg, const float* logits, const float* bias,
+                            float routed_scale, int32_t* topk_ids, float* topk_w,
+                            void* stream) {
+  moe_status st = check_config(cfg, true);
+  if (st != MOE_OK) return st;
+  if (!valid(BiasedRouting{bias, routed_scale})) return MOE_ERR_INVALID_ARG;
+  if (cfg->T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !topk_w) return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
+    return MOE_ERR_INVALID_ARG;
+  launch_route_biased(*cfg, logits, bias, routed_scale, topk_ids, topk_w, (hipStream_t)stream);
+  return launch_status();
+}
+
 moe_status moe_permute(const moe_config* cfg, const void* x, const int32_t* topk_ids,
                        void* x_perm, int32_t* seg_offsets, int32_t* seg_expert,
                        int32_t* assign_to_row, int32_t* row_to_token, int32_t* counts,
                        float* balancedness, void* workspace, size_t workspace_bytes,
                        void* stream) {
-  moe_status st = check_config(cfg);
+  moe_status st = check_config(cfg, true);
   if (st != MOE_OK) return st;
   if (cfg->T == 0) return MOE_OK;
   if (!x || !topk_ids || !x_perm || !seg_offsets || !seg_expert || !assign_to_row ||
@@ -474,7 +549,7 @@ moe_status moe_grouped_ffn_w8a8(const moe_config* cfg, const uint8_t* x_perm_q,
 moe_status moe_unpermute_combine(const moe_config* cfg, const void* y_perm,
                                  const int32_t* assign_to_row, const float* topk_w,
                                  const void* shared_y, void* out, void* stream) {
-  moe_status st = check_config(cfg);
+  moe_status st = check_config(cfg, true);
   if (st != MOE_OK) return st;
   if (cfg->T == 0) return MOE_OK;
   if (!y_perm || !assign_to_row || !out) return MOE_ERR_INVALID_ARG;
@@ -544,6 +619,89 @@ moe_status moe_quantize_fp8(int32_t n_mat, int32_t rows, int32_t cols, const voi
     return MOE_ERR_INVALID_ARG;
   launch_quantize_fp8(n_mat, rows, cols, src, q, scale, (hipStream_t)stream);
   return launch_status();
+}
+
+namespace {
+
+// The checks of a row conversion; 1: launch, 0: nothing to do, or a status.
+int check_mx_rows(int32_t dtype, int64_t rows, int32_t cols, const void* wide, const void* q,
+                  const void* scale) {
+  if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
+  if (rows < 0 || cols <= 0 || cols % 32) return MOE_ERR_INVALID_ARG;
+  // (one thread per 8 elements, 256 a workgroup, within the grid's 32 bits)
+  if (rows > ((int64_t)1 << 40) / cols) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!wide || !q || !scale || !aligned(wide, 16) || !aligned(q, 16) || !aligned(scale, 4))
+    return MOE_ERR_INVALID_ARG;
+  return 1;
+}
+
+}  // namespace
+
+moe_status moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t cols, const void* src,
+                              uint8_t* q, uint8_t* scale, void* stream) {
+  const int go = check_mx_rows(dtype, rows, cols, src, q, scale);
+  if (go <= 0) return (moe_status)go;
+  launch_quantize_mxfp4(dtype, rows * cols, src, q, scale, (hipStream_t)stream);
+  return launch_status();
+}
+
+moe_status moe_dequantize_mxfp4(int32_t dtype, int64_t rows, int32_t cols, const uint8_t* q,
+                                const uint8_t* scale, void* dst, void* stream) {
+  const int go = check_mx_rows(dtype, rows, cols, dst, q, scale);
+  if (go <= 0) return (moe_status)go;
+  launch_dequantize_mxfp4(dtype, rows * cols, q, scale, dst, (hipStream_t)stream);
+  return launch_status();
+}
+
+moe_status moe_grouped_ffn_mxfp4w(const moe_config* cfg, const void* x_perm,
+                                  const int32_t* seg_offsets, const int32_t* seg_expert,
+                                  const uint8_t* w13_q, const uint8_t* w13_scale,
+                                  const uint8_t* w2_q, const uint8_t* w2_scale,
+                                  const float* row_scale, void* y_perm, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return grouped_ffn(cfg, x_perm, nullptr, seg_offsets, seg_expert,
+                     mx_weights(w13_q, w13_scale, w2_q, w2_scale, false), row_scale, y_perm,
+                     workspace, workspace_bytes, stream);
+}
+
+moe_status moe_grouped_ffn_w4a4(const moe_config* cfg, const uint8_t* x_perm_q,
+                                const uint8_t* x_perm_scale, const int32_t* seg_offsets,
+                                const int32_t* seg_expert, const uint8_t* w13_q,
+                                const uint8_t* w13_scale, const uint8_t* w2_q,
+                                const uint8_t* w2_scale, const float* row_scale, void* y_perm,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  return grouped_ffn(cfg, x_perm_q, x_perm_scale, seg_offsets, seg_expert,
+                     mx_weights(w13_q, w13_scale, w2_q, w2_scale, true), row_scale, y_perm,
+                     workspace, workspace_bytes, stream);
+}
+
+moe_status moe_layer_forward_mxfp4w(
+    const moe_config* cfg, const float* logits, const float* route_bias, float routed_scale,
+    const void* x, const uint8_t* w13_q, const uint8_t* w13_scale, const uint8_t* w2_q,
+    const uint8_t* w2_scale, const uint8_t* shared_w13_q, const uint8_t* shared_w13_scale,
+    const uint8_t* shared_w2_q, const uint8_t* shared_w2_scale, void* out, int32_t* topk_ids,
+    float* topk_w, int32_t* counts, float* balancedness, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  const BiasedRouting b{route_bias, routed_scale};
+  return layer_forward(
+      cfg, logits, x, mx_weights(w13_q, w13_scale, w2_q, w2_scale, false),
+      mx_weights(shared_w13_q, shared_w13_scale, shared_w2_q, shared_w2_scale, false), out,
+      topk_ids, topk_w, counts, balancedness, workspace, workspace_bytes, stream, &b);
+}
+
+moe_status moe_layer_forward_w4a4(
+    const moe_config* cfg, const float* logits, const float* route_bias, float routed_scale,
+    const void* x, const uint8_t* w13_q, const uint8_t* w13_scale, const uint8_t* w2_q,
+    const uint8_t* w2_scale, const uint8_t* shared_w13_q, const uint8_t* shared_w13_scale,
+    const uint8_t* shared_w2_q, const uint8_t* shared_w2_scale, void* out, int32_t* topk_ids,
+    float* topk_w, int32_t* counts, float* balancedness, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  const BiasedRouting b{route_bias, routed_scale};
+  return layer_forward(
+      cfg, logits, x, mx_weights(w13_q, w13_scale, w2_q, w2_scale, true),
+      mx_weights(shared_w13_q, shared_w13_scale, shared_w2_q, shared_w2_scale, true), out,
+      topk_ids, topk_w, counts, balancedness, workspace, workspace_bytes, stream, &b);
 }
 
 }  // extern "C"

@@ -104,6 +104,8 @@ int32_t num_segments(const moe_config& c);
 // ---- launchers (all asynchronous on `s`) ----
 void launch_route(const moe_config& c, const float* logits, int32_t* ids, float* w,
                   hipStream_t s);
+void launch_route_biased(const moe_config& c, const float* logits, const float* bias,
+                         float routed_scale, int32_t* ids, float* w, hipStream_t s);
 void launch_permute(const moe_config& c, const void* x, const int32_t* ids, void* x_perm,
                     int32_t* seg_offsets, int32_t* seg_expert, int32_t* a2r, int32_t* r2t,
                     int32_t* counts, float* bal, const float* w, float* row_w, char* ws,
@@ -149,6 +151,14 @@ struct FfnProblem {
   // of a_deq_bytes (too small or null: the E4M3 decode tiles read the codes)
   void* a_deq;
   size_t a_deq_bytes;
+  // MXFP4 (mx = 1): w13 / w2 are E2M1 codes, half a byte each, with the E8M0
+  // scales below; mx_acts: so is A (a_e8 [A rows, K1/32]), and h is held as
+  // codes h_q [rows, Iw/2] with scales h_e8 [rows, Iw/32]
+  int32_t mx, mx_acts;
+  const uint8_t* w13_e8;  // [n_w, 2*Iw, K1/32]
+  const uint8_t* w2_e8;   // [n_w, K1, Iw/32]
+  const uint8_t* a_e8;
+  uint8_t* h_e8;
 };
 void launch_grouped_ffn(const moe_config& c, const FfnProblem* probs, int n_probs,
                         hipStream_t s);
@@ -165,6 +175,15 @@ void launch_dequantize_rows_fp8(int64_t rows, int cols, const uint8_t* q, const 
 // bf16 rows rounded through E4M3 in place: each value becomes what the
 // row quantizer's code and scale for it dequantize to.
 void launch_fake_quant_rows_fp8(int64_t rows, int cols, void* data, hipStream_t s);
+// MXFP4: n elements (a multiple of 32) of type `dtype` to E2M1 codes [n / 2]
+// and E8M0 scales [n / 32], and back.
+void launch_quantize_mxfp4(int dtype, int64_t n, const void* src, uint8_t* q, uint8_t* scale,
+                           hipStream_t s);
+void launch_dequantize_mxfp4(int dtype, int64_t n, const uint8_t* q, const uint8_t* scale,
+                             void* dst, hipStream_t s);
+// launch_grouped_ffn on MXFP4 weights (FfnProblem::mx).
+void launch_grouped_ffn_mx(const moe_config& c, const FfnProblem* probs, int n_probs,
+                           hipStream_t s);
 void launch_combine(const moe_config& c, const void* y_perm, const int32_t* a2r,
                     const float* w, const void* shared_y, void* out, hipStream_t s);
 

@@ -1,0 +1,366 @@
+"""The MXFP4 operators on the GPU against the float64 oracle: row conversion
+bit for bit, the grouped experts element by element within bounds stated in
+tests/mx_util.py."""
+import numpy as np
+import pytest
+import torch
+
+import moe_inputs as mi
+from oracle import mx as omx
+from tests import gpu_util as gu
+from tests import mx_util as mu
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe():
+    import mixture_experts_layer_segments_amd as m
+    return m
+
+
+# ------------------------------------------------------------------ rows
+def _check_rows(moe, t):
+    """Codes, scales and read-back of a device tensor, bit for bit."""
+    x = t.float().cpu().numpy().astype(np.float64)
+    c, s = omx.quantize_rows(x)
+    q, sc = mu.quantize(moe, t)
+    torch.cuda.synchronize()
+    assert (sc.cpu().numpy() == s).all(), "scales"
+    assert (q.cpu().numpy() == omx.pack(c)).all(), "codes"
+    # a block whose maximum rounds up to 4 * 2^126 = 2^128 stands for a value
+    # beyond the largest finite of either type: an infinity there
+    with np.errstate(over="ignore"):
+        ref = omx.dequantize_rows(c, s).astype(np.float32).astype(np.float64)
+    for dt in (torch.bfloat16, torch.float32):
+        back = torch.empty(t.shape, dtype=dt, device=t.device)
+        moe.moe_dequantize_mxfp4(q, sc, back)
+        got = back.float().cpu().numpy().astype(np.float64)
+        np.testing.assert_array_equal(got, ref)
+        assert (np.signbit(got) == np.signbit(ref))[~np.isnan(ref)].all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (1, 7168), (3, 96), (17, 4096), (64, 8192),
+                                       (1001, 160), (5, 65536)])
+def test_rows(moe, dtype, rows, cols):
+    rng = np.random.default_rng(rows * cols)
+    x = rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-30, 30, (rows, 1)))
+    x[rows // 2, : cols // 2] = 0
+    _check_rows(moe, torch.from_numpy(x.astype(np.float32)).to(gu.dev()).to(dtype))
+
+
+def test_rows_every_bf16_value(moe):
+    """Every bf16 bit pattern beside each of a few block maxima; infinities
+    and NaN, zeros of both signs and subnormals among them."""
+    bits = np.arange(1 << 16, dtype=np.uint16)
+    rng = np.random.default_rng(0)
+    parts = [bits, rng.permutation(bits), (bits.reshape(-1, 32).T.copy()).reshape(-1)]
+    # neighbours of every rounding border of a block with maximum 6 * 2^s
+    for s in (-126, -127, -3, 0, 100, 124):
+        v = np.linspace(-6, 6, 31 * 64)
+        blk = np.concatenate([np.full((64, 1), 6.0), v.reshape(64, 31)], 1)
+        f = np.ldexp(blk, s).astype(np.float32)
+        parts.append((f.view(np.uint32) >> 16).astype(np.uint16).reshape(-1))
+    a = np.concatenate(parts)
+    t = torch.from_numpy(a.view(np.int16)).to(gu.dev()).view(torch.bfloat16).view(-1, 32)
+    _check_rows(moe, t)
+
+
+def test_rows_fp32_borders(moe):
+    """fp32 values next to the rounding borders and to the scale's border."""
+    rng = np.random.default_rng(3)
+    borders = np.array([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], np.float32)
+    v = np.concatenate([borders, np.nextafter(borders, np.float32(0)),
+                        np.nextafter(borders[:7], np.float32(9)), -borders]).astype(np.float32)
+    blk = np.zeros((400, 32), np.float32)
+    for r in range(400):
+        blk[r] = rng.choice(v, 32) * np.exp2(np.float32(rng.integers(-126, 120)))
+    blk[0], blk[1, 7], blk[2, 31], blk[3] = 0, np.nan, -np.inf, 1e-45
+    blk[4] = np.finfo(np.float32).max
+    blk[5] = 6 * 2.0 ** -20
+    blk[5, 3] = np.nextafter(np.float32(6 * 2.0 ** -20), np.float32(1))
+    _check_rows(moe, torch.from_numpy(blk).to(gu.dev()))
+
+
+def test_rows_every_scale_reads_back(moe):
+    """All codes under all 256 scale bytes, as fp32 and as bf16."""
+    q = np.tile(np.arange(16, dtype=np.uint8) * 17, (256, 1))
+    s = np.arange(256, dtype=np.uint8).reshape(256, 1)
+    ref = omx.dequantize_rows(omx.unpack(q), s)
+    with np.errstate(over="ignore"):
+        ref32 = ref.astype(np.float32)
+    for dt in (torch.float32, torch.bfloat16):
+        back = torch.empty((256, 32), dtype=dt, device=gu.dev())
+        moe.moe_dequantize_mxfp4(mu.u8(q), mu.u8(s), back)
+        np.testing.assert_array_equal(back.float().cpu().numpy(), ref32)
+
+
+# ------------------------------------------------------------------ experts
+def _segments(lens):
+    return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32,
+                        device=gu.dev())
+
+
+def _run_ffn(moe, cfg, ex, x, lens, seg_expert, row_scale, a4, ws=None):
+    """y_perm (filled with 7 before the call) of a grouped FFN on rows x."""
+    R = moe.moe_num_rows(cfg)
+    y = torch.full((R, cfg.H), 7.0, dtype=torch.bfloat16, device=gu.dev())
+    xd = torch.zeros((R, cfg.H), dtype=torch.bfloat16, device=gu.dev())
+    xd[:x.shape[0]] = mu.to_bf16(x)
+    rs = None if row_scale is None else torch.from_numpy(row_scale).to(gu.dev())
+    if ws is None:
+        ws = gu.empty((moe.moe_workspace_size(cfg),), torch.uint8)
+    args = (_segments(lens), torch.tensor(seg_expert, dtype=torch.int32, device=gu.dev()),
+            *ex.device(), rs, y, ws)
+    if a4:
+        moe.moe_grouped_ffn_w4a4(cfg, *mu.quantize(moe, xd), *args)
+    else:
+        moe.moe_grouped_ffn_mxfp4w(cfg, xd, *args)
+    torch.cuda.synchronize()
+    return y.float().cpu().numpy().astype(np.float64)
+
+
+# segment lengths by name: a decode batch, moderate and long segments, and
+# every length around the tiles' row counts
+LENS = {
+    "one_row": [0, 1, 0, 0],
+    "decode": [3, 0, 1, 16, 2, 0, 17, 5],
+    "edges": [15, 16, 17, 31, 32, 33, 48, 49],
+    "mid": [63, 64, 65, 1, 0, 127, 128, 129],
+    "long": [300, 0, 255, 256, 257, 1, 513, 40],
+}
+SIZES = {"128x128": (128, 128), "256x384": (256, 384), "640x128": (640, 128),
+         "1152x896": (1152, 896), "2048x512": (2048, 512)}
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+@pytest.mark.parametrize("size", SIZES)
+@pytest.mark.parametrize("lens", LENS)
+def test_grouped_ffn(moe, lens, size, a4):
+    H, I = SIZES[size]
+    L = LENS[lens]
+    rng = np.random.default_rng(len(lens) * 1000 + H + I)
+    cfg = mi.MoEShape("f", T=sum(L) + 9, H=H, E=len(L), k=1, I=I)
+    ex = mu.Experts(rng, len(L), H, I)
+    n = sum(L)
+    x = mu.bf16_rows(rng, n, H)
+    rs = rng.uniform(0.1, 1.0, cfg.T).astype(np.float32) if size != "128x128" else None
+    order = rng.permutation(len(L))          # segments of any expert order
+    y = _run_ffn(moe, cfg, ex, x, L, order, rs, a4)
+    assert (y[n:] == 7).all(), "rows behind the last segment"
+    r0 = 0
+    for s, e in enumerate(order):
+        if L[s] == 0:
+            continue
+        ref, tol = mu.expert_tol(x[r0:r0 + L[s]], ex.w13[e], ex.w2[e], a4)
+        sc = 1.0 if rs is None else rs[r0:r0 + L[s], None].astype(np.float64)
+        mu.check_close(y[r0:r0 + L[s]], ref * sc, tol * sc, f"segment {s} ({L[s]} rows)")
+        r0 += L[s]
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+def test_nan_and_inf_stay_in_their_rows(moe, a4):
+    """A row with a NaN or an infinity, and an expert with NaN scales, leave
+    every other output finite and equal to the run without them; skipped
+    segments (another expert id) leave their rows alone."""
+    rng = np.random.default_rng(9)
+    L = [5, 40, 200, 3]
+    cfg = mi.MoEShape("n", T=sum(L), H=256, E=4, k=1, I=256)
+    ex = mu.Experts(rng, 4, 256, 256)
+    x = mu.bf16_rows(rng, sum(L), 256)
+    clean = _run_ffn(moe, cfg, ex, x, L, [0, 1, 2, -1], None, a4)
+    assert (clean[245:] == 7).all()
+    dirty = x.copy()
+    rows = [2, 5, 44, 45, 244]
+    dirty[rows[0], 3], dirty[rows[1], 255] = np.nan, np.inf
+    dirty[rows[2]], dirty[rows[3], 0], dirty[rows[4], 100] = np.nan, -np.inf, np.nan
+    got = _run_ffn(moe, cfg, ex, dirty, L, [0, 1, 2, -1], None, a4)
+    other = np.setdiff1d(np.arange(248), rows)
+    np.testing.assert_array_equal(got[other], clean[other])
+    assert not np.isfinite(got[rows]).all(1).any()
+    ex.s13[1, 7, 2] = 255                    # one gate row of expert 1
+    got = _run_ffn(moe, cfg, ex, x, L, [0, 1, 2, -1], None, a4)
+    np.testing.assert_array_equal(got[:5], clean[:5])
+    np.testing.assert_array_equal(got[45:], clean[45:])
+    assert np.isnan(got[5:45]).any(1).all()
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+def test_same_call_twice_is_bit_equal(moe, a4):
+    rng = np.random.default_rng(10)
+    L = [70, 300, 0, 2]
+    cfg = mi.MoEShape("n", T=sum(L), H=512, E=4, k=1, I=384)
+    ex = mu.Experts(rng, 4, 512, 384)
+    x = mu.bf16_rows(rng, sum(L), 512)
+    a = _run_ffn(moe, cfg, ex, x, L, [0, 1, 2, 3], None, a4)
+    for fill in (0, 255):                    # whatever the workspace holds
+        ws = torch.full((moe.moe_workspace_size(cfg),), fill, dtype=torch.uint8, device=gu.dev())
+        np.testing.assert_array_equal(a, _run_ffn(moe, cfg, ex, x, L, [0, 1, 2, 3], None, a4, ws))
+
+
+# ------------------------------------------------------------------ layers
+LAYERS = {
+    "decode": mi.MoEShape("l1", T=64, H=512, E=32, k=2, I=256, zipf_s=1.0, seed=61),
+    "token": mi.MoEShape("l2", T=1, H=256, E=64, k=8, I=128, score="sigmoid", n_group=8,
+                         topk_group=4, seed=62),
+    "groups_shared": mi.MoEShape("l3", T=333, H=384, E=16, k=4, I=256, score="sigmoid", n_group=4,
+                                 topk_group=2, shared_I=128, zipf_s=1.0, seed=63),
+    "softmax_groups": mi.MoEShape("l4", T=50, H=256, E=16, k=3, I=128, n_group=4, topk_group=2,
+                                  renormalize=0, seed=64),
+    "capacity": mi.MoEShape("l5", T=64, H=256, E=16, k=2, I=128, zipf_s=1.0,
+                            capacity_factor_permille=1250, seed=65),
+    "replicas": mi.MoEShape("l6", T=600, H=256, E=8, k=2, I=128, zipf_s=1.0, n_hot_split=2,
+                            split_ways=2, shared_I=256, seed=66),
+}
+
+
+def _layer_inputs(cfg):
+    rng = np.random.default_rng(cfg.seed)
+    lg = rng.standard_normal((cfg.T, cfg.E)).astype(np.float32)
+    lg -= cfg.zipf_s * 0.5 * np.log1p(np.arange(cfg.E, dtype=np.float32))
+    if cfg.T > 2:
+        lg[cfg.T // 2] = -np.inf             # a padded token: no expert
+        lg[1, 1:] = np.finfo(np.float32).min  # one expert left
+    bias = (rng.standard_normal(cfg.E) * 0.1).astype(np.float32)
+    ex = mu.Experts(rng, cfg.E, cfg.H, cfg.I)
+    sh = mu.Experts(rng, 1, cfg.H, cfg.shared_I) if cfg.shared_I else None
+    return lg, bias, mu.bf16_rows(rng, cfg.T, cfg.H), ex, sh
+
+
+class _Layer:
+    def __init__(self, moe, cfg, a4, lg, bias, x, ex, sh):
+        self.moe, self.cfg, self.a4 = moe, cfg, a4
+        self.lg = torch.from_numpy(lg).to(gu.dev())
+        self.bias = torch.from_numpy(bias).to(gu.dev())
+        self.x = mu.to_bf16(x)
+        self.w = ex.device()
+        self.sw = sh.device() if sh else (None,) * 4
+        self.out = gu.empty((cfg.T, cfg.H), torch.bfloat16)
+        self.ids = gu.empty((cfg.T, cfg.k), torch.int32)
+        self.tw = gu.empty((cfg.T, cfg.k), torch.float32)
+        self.counts = gu.empty((cfg.E,), torch.int32)
+        self.bal = gu.empty((1,), torch.float32)
+        self.ws = gu.empty((moe.moe_workspace_size(cfg),), torch.uint8)
+
+    def __call__(self):
+        f = self.moe.moe_layer_forward_w4a4 if self.a4 else self.moe.moe_layer_forward_mxfp4w
+        f(self.cfg, self.lg, self.bias, 2.5, self.x, *self.w, *self.sw, self.out, self.ids,
+          self.tw, self.counts, self.bal, self.ws)
+
+    def results(self):
+        return [t.clone() for t in (self.out, self.ids, self.tw, self.counts, self.bal)]
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+@pytest.mark.parametrize("name", LAYERS)
+def test_layer(moe, name, a4):
+    """The whole layer against the oracle, and against the same steps called
+    one by one (routing, permutation, experts, combine)."""
+    cfg = LAYERS[name]
+    lg, bias, x, ex, sh = _layer_inputs(cfg)
+    lay = _Layer(moe, cfg, a4, lg, bias, x, ex, sh)
+    lay()
+    torch.cuda.synchronize()
+    ids, w, gap = omx.route_biased(cfg, lg, bias, 2.5)
+    assert gap.min() > 1e-12
+    assert (lay.ids.cpu().numpy() == ids).all()
+    cnt = np.bincount(ids[ids >= 0], minlength=cfg.E)
+    assert (lay.counts.cpu().numpy() == cnt).all()
+    assert lay.bal.item() == np.float32(cnt.sum() / cfg.E / cnt.max())
+    # every slot's output and bound, summed in slot order; y_perm is rounded
+    # to bf16 before the combine's fp32 sum
+    ref, tol = np.zeros((cfg.T, cfg.H)), np.zeros((cfg.T, cfg.H))
+
+    def add(rows, wt, w13, w2):
+        y, tl = mu.expert_tol(x[rows], w13, w2, a4)
+        y, tl = y * wt, tl * wt
+        ref[rows] += y
+        tol[rows] += tl + mu.BF16_HALF * (np.abs(y) + tl) + 2.0 ** -22 * np.abs(y)
+    cap = cfg.T * cfg.k
+    if cfg.capacity_factor_permille:
+        cap = moe.moe_num_rows(cfg) // cfg.E
+    for e in range(cfg.E):
+        t, j = (i[:cap] for i in np.nonzero(ids == e))
+        if t.size:
+            add(t, w[t, j][:, None], ex.w13[e], ex.w2[e])
+    if sh:
+        add(np.arange(cfg.T), 1.0, sh.w13[0], sh.w2[0])
+    mu.check_close(lay.out.float().cpu().numpy(), ref, tol, name)
+    np.testing.assert_allclose(ref, omx.layer_forward(
+        cfg, ids, w, x, ex.w13, ex.w2, *((sh.w13[0], sh.w2[0]) if sh else ()), acts_fp4=a4),
+        rtol=1e-9, atol=1e-12)
+    if sh:
+        return   # (the step calls have no shared expert)
+    i2, w2 = torch.empty_like(lay.ids), torch.empty_like(lay.tw)
+    moe.moe_route_biased(cfg, lay.lg, lay.bias, 2.5, i2, w2)
+    assert torch.equal(i2, lay.ids) and torch.equal(w2, lay.tw)
+    p = gu.run_permute(moe, cfg, lay.x, i2)
+    a2r = p["a2r"].cpu().numpy()
+    rs = np.zeros(moe.moe_num_rows(cfg), np.float32)
+    rs[a2r[a2r >= 0]] = w2.cpu().numpy().reshape(-1)[a2r >= 0]
+    y = gu.empty((moe.moe_num_rows(cfg), cfg.H), torch.bfloat16)
+    args = (p["seg_offsets"], p["seg_expert"], *lay.w, torch.from_numpy(rs).to(gu.dev()), y, lay.ws)
+    if a4:
+        xp = torch.nan_to_num(p["x_perm"])   # (rows that hold no assignment)
+        moe.moe_grouped_ffn_w4a4(cfg, *mu.quantize(moe, xp), *args)
+    else:
+        moe.moe_grouped_ffn_mxfp4w(cfg, p["x_perm"], *args)
+    out = torch.empty_like(lay.out)
+    moe.moe_unpermute_combine(cfg, y, p["a2r"], None, None, out)
+    torch.cuda.synchronize()
+    assert torch.equal(out, lay.out)
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+@pytest.mark.parametrize("name", ["decode", "groups_shared", "capacity"])
+def test_layer_graph_replays_on_new_inputs(moe, name, a4):
+    """Captured once, replayed on other logits and rows with eager work in
+    between: every replay equals the eager call."""
+    cfg = LAYERS[name]
+    lg, bias, x, ex, sh = _layer_inputs(cfg)
+    lay = _Layer(moe, cfg, a4, lg, bias, x, ex, sh)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        lay()
+    torch.cuda.current_stream().wait_stream(s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lay()
+    rng = np.random.default_rng(77)
+    for _ in range(3):
+        lay.lg.copy_(torch.from_numpy(rng.standard_normal((cfg.T, cfg.E)).astype(np.float32)))
+        lay.x.copy_(mu.to_bf16(mu.bf16_rows(rng, cfg.T, cfg.H)))
+        lay.out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        got = lay.results()
+        lay.out.zero_()
+        lay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, lay.results()):
+            assert torch.equal(a, b)
+
+
+def test_two_streams_with_their_own_workspaces(moe):
+    cfg = LAYERS["decode"]
+    lays = []
+    for a4 in (False, True):
+        lays.append(_Layer(moe, cfg, a4, *_layer_inputs(cfg)))
+    for lay in lays:
+        lay()
+    torch.cuda.synchronize()
+    ref = [lay.results() for lay in lays]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for lay in lays:
+        lay.out.zero_()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for lay, s in zip(lays, streams):
+            with torch.cuda.stream(s):
+                lay()
+    torch.cuda.synchronize()
+    for lay, r in zip(lays, ref):
+        for a, b in zip(lay.results(), r):
+            assert torch.equal(a, b)
