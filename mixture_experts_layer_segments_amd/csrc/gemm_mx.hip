@@ -260,6 +260,409 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxArgs args) {
   }
 }
 
+// ---------------------------------------------------------------- ring tiles
+// Segments of more rows: BM activation rows x 256 weight rows (GEMM 1: 128
+// gate rows and the matching 128 up rows) on 8 waves, the operands copied
+// straight into an LDS ring of STAGES K stages (waits, copies and their
+// completion as in gemm.hip's ring: waves 0-3 issue, explicit vmcnt waits, a
+// plain barrier a stage).
+//
+// A stage holds, per row, 128 bytes of codes (256 elements) with FP4
+// activations, and 256 bytes of bf16 / 64 bytes of codes (128 elements) with
+// bf16 ones, in 16-byte chunks XOR-swizzled by row; then the rows' E8M0
+// bytes, as they are, in 4-byte copies.
+//
+// FP4 activations: two 16x16x128 FP4 matrix steps a stage.  Lane (r, q)
+// supplies chunk 4 s + q of row r (32 elements, one scale block) and byte
+// 4 s + q of its scales.
+// bf16 activations: lane (r, q) reads chunk q of weight row r, 32 codes and
+// one scale, and feeds them to four 16x16x32 steps, 8 at a time, against
+// chunk 4 q + m of the activation row in step m.
+template <bool AF4, int BM, int STAGES, int WAVES_M>
+struct MxRing {
+  static constexpr int BN = 256, NTHR = 512, NI = 4;
+  static constexpr int BK = AF4 ? 256 : 128;              // elements of a stage
+  static constexpr int KCA = AF4 ? 8 : 16, KCB = AF4 ? 8 : 4;   // chunks per row
+  static constexpr int RPA = 64 / KCA, RPB = 64 / KCB;    // rows per 1 KiB copy
+  static constexpr int SD = BK / 128;                     // scale dwords per row
+  static constexpr int SRP = 64 / SD;                     // rows per scale copy
+  static constexpr int A_CH = BM * KCA, B_CH = BN * KCB;
+  static constexpr int AS_DW = AF4 ? BM * SD : 0, BS_DW = BN * SD;
+  // 16-byte chunks of a stage, scales included
+  static constexpr int STAGE_CH = A_CH + B_CH + (AS_DW + BS_DW) / 4;
+  static constexpr int RING_CH = STAGES * STAGE_CH;
+  static constexpr int A_IT = BM / RPA / NI, B_IT = BN / RPB / NI;
+  static constexpr int S_N = (AS_DW + BS_DW) / 64;        // scale copies of a stage
+  static constexpr int AS_N = AS_DW / 64;                 //   of them activations'
+  static constexpr int S_IT = (S_N + NI - 1) / NI;
+  static constexpr int LPI = A_IT + B_IT + S_IT;          // copies per issuing wave
+  static constexpr int WAVES_N = 8 / WAVES_M;
+  static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
+  static constexpr int TM = WM / 16, TN = WN / 16;
+  // weights that no other row tile reads again stream past the caches, where
+  // a row's piece is a whole 128-byte line
+  static constexpr int B_AUX = (AF4 && BM < 256) ? kAuxNT : 0;
+  static_assert((BM / RPA) % NI == 0 && (BN / RPB) % NI == 0, "copy blocks per wave");
+  static_assert(LPI * (STAGES - 2) < 64, "vmcnt range");
+};
+
+template <typename R>
+struct MxTile {
+  int r0, len, e, m0, n0;
+  bool stream;
+  const MxProblem* P;
+  __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
+  uint32_t voff[R::LPI];
+};
+
+template <int MODE, bool AF4, typename R, int BM>
+__device__ __forceinline__ void mx_ring_setup(const MxArgs& args, const int* tiles_l, int tile,
+                                              MxTile<R>& t) {
+  const int lane = threadIdx.x & 63;
+  const int wvs = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  int lo = 0, hi = args.n_seg_total - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (tiles_l[mid] <= tile) lo = mid; else hi = mid - 1;
+  }
+  const int pi = lo < args.p[0].n_seg ? 0 : 1;
+  const MxProblem& P = args.p[pi];
+  t.P = &P;
+  t.r0 = 0;
+  t.len = P.rows;
+  t.e = 0;
+  if (P.seg_offsets) {
+    const int s = lo - (pi ? args.p[0].n_seg : 0);
+    t.r0 = P.seg_offsets[s];
+    t.len = P.seg_offsets[s + 1] - t.r0;
+    t.e = P.seg_expert[s];
+  }
+  const int mt = (t.len + BM - 1) / BM;
+  t.stream = mt == 1;
+  constexpr int ncols = MODE == 0 ? R::BN / 2 : R::BN;
+  const int K = P.K, N = P.N;
+  const int nt = (N + ncols - 1) / ncols;
+  const int local = tile - tiles_l[lo];
+  const int grp = local / (kGroupM * nt);
+  const int first_m = grp * kGroupM;
+  const int gm = min(kGroupM, mt - first_m);
+  const int lg = local - grp * kGroupM * nt;
+  t.m0 = (first_m + lg % gm) * BM;
+  t.n0 = (lg / gm) * ncols;
+  const uint32_t arow_b = AF4 ? K / 2 : K * 2, brow_b = K / 2, srow_b = K / 32;
+  const int64_t e_row = (int64_t)t.e * P.b_rows;
+  t.ra = buffer_rsrc(P.A, (uint32_t)((size_t)P.a_ld_rows * arow_b));
+  t.rb = buffer_rsrc(P.B + e_row * brow_b, (uint32_t)((size_t)P.b_rows * brow_b));
+  if constexpr (AF4) t.rsa = buffer_rsrc(P.a_e8, (uint32_t)((size_t)P.a_ld_rows * srow_b));
+  t.rsb = buffer_rsrc(P.b_e8 + e_row * srow_b, (uint32_t)((size_t)P.b_rows * srow_b));
+  if (wvs >= R::NI) return;
+  auto a_src = [&](int row) -> uint32_t {
+    const int ar = t.r0 + min(t.m0 + row, t.len - 1);
+    return P.a_rows ? P.a_rows[ar] : ar;
+  };
+  auto b_src = [&](int br) -> uint32_t {
+    if (MODE == 0) {
+      const int col = min(t.n0 + (br % (R::BN / 2)), N - 1);
+      return br < R::BN / 2 ? col : P.up_off + col;
+    }
+    return min(t.n0 + br, N - 1);
+  };
+#pragma unroll
+  for (int i = 0; i < R::LPI; ++i) {
+    if (i < R::A_IT) {
+      const int row = (i * R::NI + wvs) * R::RPA + lane / R::KCA;
+      t.voff[i] = a_src(row) * arow_b + ((lane % R::KCA) ^ swz<R::KCA>(row)) * 16;
+    } else if (i < R::A_IT + R::B_IT) {
+      const int br = ((i - R::A_IT) * R::NI + wvs) * R::RPB + lane / R::KCB;
+      t.voff[i] = b_src(br) * brow_b + ((lane % R::KCB) ^ swz<R::KCB>(br)) * 16;
+    } else {
+      // (a copy past the last repeats it: every wave issues the same number)
+      const int c = min((i - R::A_IT - R::B_IT) * R::NI + wvs, R::S_N - 1);
+      const int row = c * R::SRP + lane / R::SD;
+      t.voff[i] = (row < R::AS_N * R::SRP ? a_src(row) : b_src(row - R::AS_N * R::SRP)) * srow_b +
+                  (lane % R::SD) * 4;
+    }
+  }
+}
+
+// This wave's copies of K stage kt.  (A last stage that reaches past K reads
+// on into the next row, or zeros past the buffer: those elements enter no
+// product.)
+template <bool AF4, typename R, int STAGES, int AUX>
+__device__ __forceinline__ void mx_ring_issue(const MxTile<R>& t, u32x4* ring, int kt, int wv) {
+  u32x4* slot = ring + (kt % STAGES) * R::STAGE_CH;
+#pragma unroll
+  for (int i = 0; i < R::LPI; ++i) {
+    if (i < R::A_IT) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(t.ra, MOE_LDS_PTR(slot + (i * R::NI + wv) * 64), 16,
+                                               t.voff[i], kt * (R::KCA * 16), 0, 0);
+    } else if (i < R::A_IT + R::B_IT) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          t.rb, MOE_LDS_PTR(slot + R::A_CH + ((i - R::A_IT) * R::NI + wv) * 64), 16, t.voff[i],
+          kt * (R::KCB * 16), 0, AUX);
+    } else {
+      const int c = min((i - R::A_IT - R::B_IT) * R::NI + wv, R::S_N - 1);
+      u32x4* dst = slot + R::A_CH + R::B_CH + c * 16;
+      if (AF4 && (R::AS_N % R::NI == 0 ? (i - R::A_IT - R::B_IT) * R::NI < R::AS_N : c < R::AS_N))
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(t.rsa, MOE_LDS_PTR(dst), 4, t.voff[i],
+                                                 kt * (R::SD * 4), 0, 0);
+      else
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(t.rsb, MOE_LDS_PTR(dst), 4, t.voff[i],
+                                                 kt * (R::SD * 4), 0, 0);
+    }
+  }
+}
+
+template <bool AF4, typename R, int STAGES>
+__device__ __forceinline__ void mx_ring_stage(const MxTile<R>& t, u32x4* ring, int kt, int wv) {
+  if (R::B_AUX && t.stream) mx_ring_issue<AF4, R, STAGES, R::B_AUX>(t, ring, kt, wv);
+  else mx_ring_issue<AF4, R, STAGES, 0>(t, ring, kt, wv);
+}
+
+__device__ __forceinline__ i32x8 fp4_operand(u32x4 v) {
+  return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
+}
+
+// One stage's matrix products.  `half`: only the stage's first 128 elements
+// lie inside K (FP4 activations).
+// (Fragment rows are r plus multiples of 16, so the swizzle is r's, and the
+// fragments of a wave lie at constant distances.)
+template <int MODE, bool AF4, typename R>
+__device__ __forceinline__ void mx_ring_mma(const u32x4* slot, int wm, int wn, int lane, bool half,
+                                            f32x4 (&acc)[R::TM][R::TN]) {
+  constexpr int TM = R::TM, TN = R::TN;
+  const int r = lane & 15, q = lane >> 4;
+  const int arow = wm * R::WM + r;
+  const int brow = wn * (MODE == 0 ? R::WN / 2 : R::WN) + r;
+  // weight rows of fragment ni from brow
+  auto b_at = [](int ni) constexpr {
+    return MODE == 1 || ni < TN / 2 ? ni * 16 : R::BN / 2 + (ni - TN / 2) * 16;
+  };
+  const u32x4* As = slot + arow * R::KCA;
+  const u32x4* Bs = slot + R::A_CH + brow * R::KCB;
+  const uint32_t* sc = reinterpret_cast<const uint32_t*>(slot + R::A_CH + R::B_CH);
+  if constexpr (AF4) {
+    const u32x2* sa2 = reinterpret_cast<const u32x2*>(sc);
+    const u32x2* sb2 = reinterpret_cast<const u32x2*>(sc + R::AS_DW);
+    // bytes q and 4 + q of a row's eight
+    const uint32_t sel = (uint32_t)q | (uint32_t)(4 + q) << 8;
+    int sa[TM], sb[TN];
+#pragma unroll
+    for (int mi = 0; mi < TM; ++mi) {
+      const u32x2 v = sa2[arow + mi * 16];
+      sa[mi] = (int)__builtin_amdgcn_perm(v.y, v.x, sel);
+    }
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni) {
+      const u32x2 v = sb2[brow + b_at(ni)];
+      sb[ni] = (int)__builtin_amdgcn_perm(v.y, v.x, sel);
+    }
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if (s == 1 && half) break;
+      i32x8 af[TM], bq[TN];
+#pragma unroll
+      for (int mi = 0; mi < TM; ++mi)
+        af[mi] = fp4_operand(As[mi * 16 * R::KCA + ((s * 4 + q) ^ swz<R::KCA>(r))]);
+#pragma unroll
+      for (int ni = 0; ni < TN; ++ni)
+        bq[ni] = fp4_operand(Bs[b_at(ni) * R::KCB + ((s * 4 + q) ^ swz<R::KCB>(r))]);
+      // weights as the first operand: lane l gets output row l % 16 and
+      // columns 4 (l / 16) .. +3 of each 16 x 16 piece
+#pragma unroll
+      for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi)
+          acc[mi][ni] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                     bq[ni], af[mi], acc[mi][ni], 4, 4, 0, sb[ni], 0, sa[mi])
+                               : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                     bq[ni], af[mi], acc[mi][ni], 4, 4, 1, sb[ni], 1, sa[mi]);
+      // (the second step's operands are not read before the first's are used:
+      // the 256-row tile's accumulators leave no room for both)
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+    u32x4 bc[TN];
+    float bs[TN];
+#pragma unroll
+    for (int ni = 0; ni < TN; ++ni) {
+      bc[ni] = Bs[b_at(ni) * R::KCB + (q ^ swz<R::KCB>(r))];
+      bs[ni] = e8m0_float((sc[brow + b_at(ni)] >> (8 * q)) & 0xffu);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      bf16x8 af[TM], bq[TN];
+#pragma unroll
+      for (int mi = 0; mi < TM; ++mi)
+        af[mi] = __builtin_bit_cast(bf16x8,
+                                    As[mi * 16 * R::KCA + ((4 * q + m) ^ swz<R::KCA>(r))]);
+#pragma unroll
+      for (int ni = 0; ni < TN; ++ni)
+        bq[ni] = __builtin_bit_cast(bf16x8, e2m1x8_to_bf16(bc[ni][m], bs[ni]));
+#pragma unroll
+      for (int ni = 0; ni < TN; ++ni)
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi)
+          acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bq[ni], af[mi], acc[mi][ni], 0, 0,
+                                                                0);
+    }
+  }
+}
+
+// The tile's output: every wave stages its rows in its own part of the idle
+// ring, chunk c of row rr at c ^ (rr % CPR), and whole 16-byte row chunks go
+// out; a chunk past the segment or past N takes an offset beyond the store's
+// range and is dropped.  GEMM 1 with FP4 activations: after a barrier, 16
+// lanes take one row's 128 columns of h, 4 lanes a 1 x 32 block, and write
+// its codes (64 contiguous bytes a row) and scales.
+template <int MODE, bool AF4, typename R>
+__device__ __forceinline__ void mx_ring_store(const MxTile<R>& t, const u32x2* out, u32x4* ring) {
+  constexpr int TM = R::TM, WM = R::WM, NPM = MODE == 0 ? R::TN / 2 : R::TN;
+  constexpr int COUT = MODE == 0 ? R::WN / 2 : R::WN;
+  constexpr int CPR = COUT / 8, RPI = 64 / CPR;
+  static_assert(CPR <= 16 && 64 % CPR == 0 && WM % RPI == 0, "output transpose shape");
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));   // (addresses formed here, not kept through the K loop)
+  const int wv = threadIdx.x >> 6;
+  const int wm = wv / R::WAVES_N, wn = wv % R::WAVES_N;
+  u32x4* reg = ring + (size_t)wv * WM * CPR;
+#pragma unroll
+  for (int mi = 0; mi < TM; ++mi) {
+    const int rr = mi * 16 + (lane & 15);
+#pragma unroll
+    for (int ni = 0; ni < NPM; ++ni) {
+      const int c = ni * 2 + ((lane >> 4) >> 1);
+      reinterpret_cast<u32x2*>(reg + rr * CPR + (c ^ (rr % CPR)))[(lane >> 4) & 1] =
+          out[mi * NPM + ni];
+    }
+  }
+  const MxProblem& P = *t.P;
+  const int N = P.N;
+  if constexpr (MODE == 0 && AF4) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    raw_barrier();   // every wave's rows are staged
+    constexpr int BM = WM * (8 / R::WAVES_N);
+    const __amdgpu_buffer_rsrc_t rq =
+        buffer_rsrc(P.Cq + (size_t)t.r0 * (N / 2), (uint32_t)((size_t)t.len * (N / 2)));
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int cc = tid & 15;                          // this lane's 8 of the 128 columns
+    const int swn = cc / CPR, sc = cc % CPR;
+#pragma unroll
+    for (int it = 0; it < BM / 32; ++it) {
+      const int row = it * 32 + (tid >> 4);
+      const int swm = row / WM, rr = row % WM;
+      const u32x4 v = ring[(size_t)(swm * R::WAVES_N + swn) * WM * CPR + rr * CPR + (sc ^ (rr % CPR))];
+      float f[8];
+      uint32_t a = 0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        f[2 * j] = __uint_as_float(v[j] << 16);
+        f[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+        a = max(a, max(__float_as_uint(f[2 * j]) & 0x7fffffffu,
+                       __float_as_uint(f[2 * j + 1]) & 0x7fffffffu));
+      }
+      a = max(a, (uint32_t)wave_dev::dpp<0xB1>((int)a));
+      a = max(a, (uint32_t)wave_dev::dpp<0x4E>((int)a));
+      const uint32_t b = block_e8m0(a);
+      const uint32_t codes = e2m1x8(f, b);
+      const int grow = t.m0 + row;
+      const uint32_t off = grow < t.len
+                               ? ((uint32_t)grow * (uint32_t)N + (uint32_t)(t.n0 + cc * 8)) / 2u
+                               : 0xFFFFFFF0u;
+      __builtin_amdgcn_raw_buffer_store_b32(codes, rq, off, 0, 0);
+      if ((cc & 3) == 0 && grow < t.len)
+        P.c_e8[(size_t)(t.r0 + grow) * (N / 32) + (t.n0 + cc * 8) / 32] = (uint8_t)b;
+    }
+  } else {
+    const __amdgpu_buffer_rsrc_t rc =
+        buffer_rsrc(P.C + (size_t)t.r0 * N, (uint32_t)((size_t)t.len * N * 2));
+    const int col0 = t.n0 + wn * COUT;
+#pragma unroll
+    for (int it = 0; it < WM / RPI; ++it) {
+      const int rr = it * RPI + lane / CPR, c = lane % CPR;
+      const u32x4 v = reg[rr * CPR + (c ^ (rr % CPR))];
+      const int row = t.m0 + wm * WM + rr, col = col0 + c * 8;
+      const uint32_t off = (row < t.len && col < N)
+                               ? ((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u
+                               : 0xFFFFFFF0u;
+      __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, MODE == 1 ? kAuxNT : 0);
+    }
+  }
+}
+
+template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
+__global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
+  using R = MxRing<AF4, BM, STAGES, WAVES_M>;
+  constexpr int TM = R::TM, TN = R::TN, NPM = MODE == 0 ? TN / 2 : TN;
+  // (the ring and the tile table are the only LDS objects, as in gemm.hip's
+  // ring kernel; the table's scan borrows the idle ring)
+  __shared__ __attribute__((aligned(1024))) u32x4 ring[R::RING_CH];
+  extern __shared__ int tiles_l[];
+  build_tile_table<512>(args, tiles_l, reinterpret_cast<int*>(ring), args.tile_bm,
+                        args.tile_ncols, args.min_len, args.max_len);
+  const int total = tiles_l[args.n_seg_total];
+  const int lane = threadIdx.x & 63;
+  const int wvs = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wvs / R::WAVES_N, wn = wvs % R::WAVES_N;
+  const int G = gridDim.x;
+  for (int tile = xcd_logical(blockIdx.x, G); tile < total; tile += G) {
+    MxTile<R> t;
+    mx_ring_setup<MODE, AF4, R, BM>(args, tiles_l, tile, t);
+    raw_barrier();   // the previous tile's output has left the ring
+    const int K = t.P->K, KT = (K + R::BK - 1) / R::BK;
+    if (wvs < R::NI) {
+#pragma unroll
+      for (int st = 0; st < STAGES - 1; ++st)
+        if (st < KT) mx_ring_stage<AF4, R, STAGES>(t, ring, st, wvs);
+    }
+    u32x2 outv[TM * NPM];
+    {
+      f32x4 acc[TM][TN];
+#pragma unroll
+      for (int mi = 0; mi < TM; ++mi)
+#pragma unroll
+        for (int ni = 0; ni < TN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
+      // a wave whose rows all lie past the segment takes part in the copies
+      // and barriers only
+      const bool rows_here = t.m0 + wm * R::WM < t.len;
+      int kt = 0;
+      do {   // (K >= 128: at least one stage; a loop that may run none held a
+             // second set of output registers, with spills)
+        if (wvs < R::NI) wait_stages<R::LPI, STAGES - 2>(min(STAGES - 2, KT - 1 - kt));
+        raw_barrier();
+        if (kt + STAGES - 1 < KT && wvs < R::NI)
+          mx_ring_stage<AF4, R, STAGES>(t, ring, kt + STAGES - 1, wvs);
+        if (!rows_here) continue;
+        mx_ring_mma<MODE, AF4, R>(ring + (kt % STAGES) * R::STAGE_CH, wm, wn, lane,
+                                  AF4 && kt * R::BK + 128 >= K, acc);
+      } while (++kt < KT);
+#pragma unroll
+      for (int mi = 0; mi < TM; ++mi) {
+        float rs = 1.0f;
+        if (MODE == 1 && t.P->scale) {
+          const int row = t.m0 + wm * R::WM + mi * 16 + (lane & 15);
+          rs = t.P->scale[t.r0 + min(row, t.len - 1)];
+        }
+#pragma unroll
+        for (int ni = 0; ni < NPM; ++ni) {
+          if (MODE == 0) {
+            const f32x4 g = acc[mi][ni], u = acc[mi][ni + TN / 2];
+            outv[mi * NPM + ni] = u32x2{pack_bf16x2(silu(g[0]) * u[0], silu(g[1]) * u[1]),
+                                        pack_bf16x2(silu(g[2]) * u[2], silu(g[3]) * u[3])};
+          } else {
+            const f32x4 y = acc[mi][ni];
+            outv[mi * NPM + ni] =
+                u32x2{pack_bf16x2(y[0] * rs, y[1] * rs), pack_bf16x2(y[2] * rs, y[3] * rs)};
+          }
+        }
+      }
+    }
+    raw_barrier();   // every wave is done reading the ring: it takes the output
+    mx_ring_store<MODE, AF4, R>(t, outv, ring);
+  }
+}
+
 MxArgs cover(MxArgs g, int bm, int ncols, int min_len, int max_len) {
   g.tile_bm = bm;
   g.tile_ncols = ncols;
@@ -276,14 +679,38 @@ void launch_stream(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
       cover(g, 16, 16 * TN / (MODE == 0 ? 2 : 1), min_len, max_len));
 }
 
-template <bool AF4>
-void launch_pair(const MxArgs& g1, const MxArgs& g2, hipStream_t s) {
+template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
+void launch_ring(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
+  auto k = mx_ring_kernel<MODE, AF4, BM, STAGES, WAVES_M>;
+  const size_t dyn = (size_t)(g.n_seg_total + 1) * sizeof(int);
+  k<<<persistent_grid(k, dyn, 1, 512), 512, dyn, s>>>(
+      cover(g, BM, MODE == 0 ? 128 : 256, min_len, max_len));
+}
+
+// A ring launch over the segments of [min_len, max_len) rows, on STAGES
+// stages if the tile table fits beside them, else on two.
+template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
+void launch_ring_fit(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
+  const size_t ring = (size_t)MxRing<AF4, BM, STAGES, WAVES_M>::RING_CH * 16;
+  if (ring + (size_t)(g.n_seg_total + 1) * sizeof(int) + 64 <= kMaxLdsBytes)
+    launch_ring<MODE, AF4, BM, STAGES, WAVES_M>(g, min_len, max_len, s);
+  else
+    launch_ring<MODE, AF4, BM, 2, WAVES_M>(g, min_len, max_len, s);
+}
+
+template <int MODE, bool AF4>
+void launch_gemm(const MxArgs& g, bool few_rows, int longest, hipStream_t s) {
+  if (few_rows) {
+    launch_stream<MODE, AF4, MODE == 0 && AF4 ? 4 : 2, 2>(g, 1, kAll, s);
+    return;
+  }
+  constexpr int kSmall = 64, kBig = 256;
+  launch_ring_fit<MODE, AF4, 64, 3, 2>(g, 1, kSmall + 1, s);
   if constexpr (AF4) {
-    launch_stream<0, true, 4, 2>(g1, 1, kAll, s);
-    launch_stream<1, true, 2, 2>(g2, 1, kAll, s);
+    launch_ring_fit<MODE, AF4, 128, 3, 2>(g, kSmall + 1, kBig, s);
+    if (longest >= kBig) launch_ring_fit<MODE, AF4, 256, 2, 4>(g, kBig, kAll, s);
   } else {
-    launch_stream<0, false, 2, 2>(g1, 1, kAll, s);
-    launch_stream<1, false, 2, 2>(g2, 1, kAll, s);
+    launch_ring_fit<MODE, AF4, 128, 3, 2>(g, kSmall + 1, kAll, s);
   }
 }
 
@@ -334,8 +761,20 @@ void launch_grouped_ffn_mx(const moe_config& c, const FfnProblem* probs, int n_p
   }
   g1.n_probs = g2.n_probs = n_probs;
   g1.n_seg_total = g2.n_seg_total = nst;
-  if (probs[0].mx_acts) launch_pair<true>(g1, g2, s);
-  else launch_pair<false>(g1, g2, s);
+  int64_t rows = 0;
+  int longest = 0;
+  for (int p = 0; p < n_probs; ++p) {
+    rows += probs[p].rows;
+    longest = probs[p].max_seg_rows > longest ? probs[p].max_seg_rows : longest;
+  }
+  const bool few = uses_decode_tiles(rows, nst);
+  if (probs[0].mx_acts) {
+    launch_gemm<0, true>(g1, few, longest, s);
+    launch_gemm<1, true>(g2, few, longest, s);
+  } else {
+    launch_gemm<0, false>(g1, few, longest, s);
+    launch_gemm<1, false>(g2, few, longest, s);
+  }
   MOE_DBG("grouped gemms (MXFP4)");
 }
 
