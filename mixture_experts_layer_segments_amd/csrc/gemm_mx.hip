@@ -43,112 +43,118 @@ struct MxArgs {
 
 // ---------------------------------------------------------------- streaming tiles
 // Segments of a few rows: the time is that of reading every active expert's
-// codes once (17/32 byte a weight), so the codes go straight from memory to
-// the matrix operands, with no LDS and no barrier between a wave's loads.
+// codes once (17/32 byte a weight).
 //
 // Tile: 16 activation rows x 16 TN weight rows (GEMM 1: the first half gate
-// rows, the second the matching up rows); the four waves of a workgroup split
-// K and add their partial sums through LDS at the end.  Work along K goes in
-// 128-element slabs.  Of a slab, lane (r, q) = (lane % 16, lane / 16) holds
-// elements 32 q .. 32 q + 31 of row r: 16 bytes of codes, one whole scale
-// block, loaded by one 16-byte access (the four lanes of a row cover 64
-// contiguous bytes, two slabs a 128-byte line).  That is the operand layout of
-// the 16x16x128 FP4 matrix instruction; for bf16 activations four 16x16x32
-// instructions take the 32 elements in four steps of 8, the activation
-// fragment of the same elements beside it (a sum over K is a sum in any
-// order).
-// A unit: SL slabs of one wave.  Wave w takes units w, w + 4, ... of K, so the
-// four waves read 4 SL * 64 contiguous bytes of every row together.
-template <bool AF4, int TN, int SL>
-struct MxUnit {
-  u32x4 w[TN][SL];                     // weight codes
-  uint32_t ws[TN][SL];                 // their 4 scale bytes a slab, byte q this lane's
-  u32x4 a[SL][AF4 ? 1 : 4];            // activations
-  uint32_t as[AF4 ? SL : 1];
+// rows, the second the matching up rows), on KS waves that split K and add
+// their partial sums through LDS (a workgroup is 4 / KS tiles).  A stage is
+// 256 elements of K, 128 bytes of codes a row: a load instruction reads whole
+// 128-byte lines of 8 rows (reading 64-byte pieces of 16 rows, the matrix
+// operand's own layout, held the kernel to 3.3 TB/s), each wave turns the
+// stage through LDS of its own (no barrier in the K loop) and keeps the next
+// four stages' codes and activations in flight in registers.
+//
+// Of a stage's two 128-element slabs, lane (r, q) = (lane % 16, lane / 16)
+// takes elements 32 q .. 32 q + 31 of row r: 16 bytes of codes, one whole
+// scale block.  That is the operand layout of the 16x16x128 FP4 matrix
+// instruction; for bf16 activations four 16x16x32 instructions take the 32
+// elements in four steps of 8, the activation fragment of the same elements
+// beside it (a sum over K is a sum in any order).  The E8M0 bytes come four
+// stages (32 bytes a row) at a time and go through LDS too.
+constexpr int kMxDepth = 4;   // stages in flight
+
+// Byte offsets of a lane's operands at the wave's first stage; the stage goes
+// in the scalar offset.
+struct MxSrc {
+  __amdgpu_buffer_rsrc_t rb, rs, ra, ras;
+  uint32_t w, ws, a, as;
+  uint32_t w8;              // 8 weight rows further, in bytes
+  uint32_t up;              // GEMM 1: from a gate row to its up row, in bytes
+  uint32_t ws_up;           // the same, in scale bytes
 };
 
-template <bool AF4, int TN, int SL>
-__device__ __forceinline__ void mx_load_a(MxUnit<AF4, TN, SL>& u, const MxProblem& P, bool ok,
-                                          uint32_t arow, int slab0, int nslab, int q) {
+// Orders a wave's LDS accesses between its own lanes (they execute in order;
+// this keeps the compiler from moving a read over another lane's write).
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+}
+
+template <bool AF4>
+struct MxActs {
+  u32x4 v[2][AF4 ? 1 : 4];
+  u32x2 s;                  // FP4: the row's 8 scale bytes of the stage
+};
+
+template <bool AF4>
+__device__ __forceinline__ void mx_load_a(MxActs<AF4>& a, const MxSrc& s, int stage) {
+  if constexpr (AF4) {
+    a.v[0][0] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a, stage * 128, 0);
+    a.v[1][0] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a + 64, stage * 128, 0);
+    a.s = __builtin_amdgcn_raw_buffer_load_b64(s.ras, s.as, stage * 8, 0);
+  } else {
 #pragma unroll
-  for (int i = 0; i < SL; ++i) {
-    const int sl = slab0 + i;
-    const bool in = ok && sl < nslab;
-    if constexpr (AF4) {
-      const uint8_t* a = (const uint8_t*)P.A + (size_t)arow * (P.K / 2);
-      u.a[i][0] = in ? *reinterpret_cast<const u32x4*>(a + sl * 64 + q * 16) : u32x4{0, 0, 0, 0};
-      u.as[i] = in ? *reinterpret_cast<const uint32_t*>(P.a_e8 + (size_t)arow * (P.K / 32) + sl * 4)
-                   : 0u;
-    } else {
-      const uint16_t* a = (const uint16_t*)P.A + (size_t)arow * P.K + sl * 128 + q * 32;
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        u.a[i][j] = in ? reinterpret_cast<const u32x4*>(a)[j] : u32x4{0, 0, 0, 0};
-    }
+        a.v[i][j] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a + i * 256 + j * 16,
+                                                          stage * 512, 0);
   }
 }
 
-template <bool AF4, int TN, int SL>
-__device__ __forceinline__ void mx_load_w(MxUnit<AF4, TN, SL>& u, const uint8_t* Bb,
-                                          const uint8_t* Sb, const uint32_t (&brow)[TN], int K,
-                                          int slab0, int nslab, int q) {
+template <int MODE, int TN>
+__device__ __forceinline__ void mx_load_w(u32x4 (&w)[2 * TN], const MxSrc& s, int stage) {
 #pragma unroll
-  for (int i = 0; i < SL; ++i) {
-    const int sl = slab0 + i;
-    if (sl < nslab) {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        u.w[j][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(
-            Bb + (size_t)(brow[j] * (uint32_t)(K / 2)) + sl * 64 + q * 16));
-        u.ws[j][i] = *reinterpret_cast<const uint32_t*>(
-            Sb + (size_t)(brow[j] * (uint32_t)(K / 32)) + sl * 4);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        u.w[j][i] = u32x4{0, 0, 0, 0};
-        u.ws[j][i] = 0;
-      }
-    }
+  for (int i = 0; i < 2 * TN; ++i) {
+    const bool up = MODE == 0 && i >= TN;
+    w[i] = __builtin_amdgcn_raw_buffer_load_b128(
+        s.rb, s.w, stage * 128 + (up ? s.up + (i - TN) * s.w8 : i * s.w8), kAuxNT);
   }
 }
 
-template <bool AF4, int TN, int SL>
-__device__ __forceinline__ void mx_unit_mma(const MxUnit<AF4, TN, SL>& u, f32x4 (&acc)[TN],
-                                            int q) {
+// One stage's products: the codes in `wl` (16 TN rows of 8 chunks, chunk c at
+// c ^ swz<8>(row)), this stage's scale dwords at `sl` (8 dwords a row),
+// `slabs` of its two slabs inside K.
+template <bool AF4, int TN>
+__device__ __forceinline__ void mx_stage_mma(const u32x4* wl, const uint32_t* sl,
+                                             const MxActs<AF4>& a, int slabs, int r, int q,
+                                             f32x4 (&acc)[TN]) {
 #pragma unroll
-  for (int i = 0; i < SL; ++i) {
-    if constexpr (AF4) {
-      const u32x4 av = u.a[i][0];
-      const i32x8 a = {(int)av[0], (int)av[1], (int)av[2], (int)av[3], 0, 0, 0, 0};
-      const int sa = (int)(u.as[i] >> (8 * q));
+  for (int i = 0; i < 2; ++i) {
+    if (i >= slabs) break;
 #pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const u32x4 wv = u.w[j][i];
-        const i32x8 b = {(int)wv[0], (int)wv[1], (int)wv[2], (int)wv[3], 0, 0, 0, 0};
+    for (int j = 0; j < TN; ++j) {
+      const u32x4 w = wl[(j * 16 + r) * 8 + ((4 * i + q) ^ swz<8>(r))];
+      const uint32_t sb = sl[(j * 16 + r) * 8 + i] >> (8 * q);
+      if constexpr (AF4) {
+        const u32x4 v = a.v[i][0];
         acc[j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-            a, b, acc[j], 4, 4, 0, sa, 0, (int)(u.ws[j][i] >> (8 * q)));
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < TN; ++j) {
-        const float sc = e8m0_float((u.ws[j][i] >> (8 * q)) & 0xffu);
+            i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0},
+            i32x8{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0}, acc[j], 4, 4, 0,
+            (int)(a.s[i] >> (8 * q)), 0, (int)sb);
+      } else {
+        const float sc = e8m0_float(sb & 0xffu);
 #pragma unroll
         for (int m = 0; m < 4; ++m)
           acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-              __builtin_bit_cast(bf16x8, u.a[i][m]),
-              __builtin_bit_cast(bf16x8, e2m1x8_to_bf16(u.w[j][i][m], sc)), acc[j], 0, 0, 0);
+              __builtin_bit_cast(bf16x8, a.v[i][m]),
+              __builtin_bit_cast(bf16x8, e2m1x8_to_bf16(w[m], sc)), acc[j], 0, 0, 0);
       }
     }
   }
 }
 
-template <int MODE, bool AF4, int TN, int SL>
-__global__ __launch_bounds__(256) void mx_stream_kernel(MxArgs args) {
+template <int MODE, bool AF4, int TN, int KS, int WPE>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(WPE)))
+void mx_stream_kernel(MxArgs args) {
   constexpr int NCOLS = 16 * TN / (MODE == 0 ? 2 : 1);   // output columns of a tile
+  constexpr int NT = 4 / KS;                             // tiles of a workgroup
   static_assert(128 % NCOLS == 0, "whole tiles along N (a multiple of 128)");
   static_assert(!(MODE == 0 && AF4) || NCOLS == 32, "a tile holds h's whole 1 x 32 blocks");
-  __shared__ f32x4 red[4][TN][64];
+  // a wave's turn buffer: two stages of codes, then four stages' scales
+  constexpr int WB_CH = 2 * 16 * TN * 8, WS_CH = 16 * TN * 2;
+  __shared__ u32x4 turn[4][WB_CH + WS_CH];
+  __shared__ f32x4 red[KS > 1 ? 4 : 1][KS > 1 ? TN : 1][64];
   __shared__ int wsum[256 / 64 + 1];
   extern __shared__ int tiles_l[];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -157,64 +163,138 @@ __global__ __launch_bounds__(256) void mx_stream_kernel(MxArgs args) {
   build_tile_table<256>(args, tiles_l, wsum, args.tile_bm, args.tile_ncols, args.min_len,
                         args.max_len);
   const int total = tiles_l[nst];
-  const int G = gridDim.x;
   const int r = lane & 15, q = lane >> 4;
+  const int ks = wv % KS;
 
-  for (int tile = xcd_logical(blockIdx.x, G); tile < total; tile += G) {
-    int lo = 0, hi = nst - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (tiles_l[mid] <= tile) lo = mid; else hi = mid - 1;
-    }
-    const int pi = lo < args.p[0].n_seg ? 0 : 1;
-    const MxProblem& P = args.p[pi];
-    int r0 = 0, len = P.rows, e = 0;
-    if (P.seg_offsets) {
-      const int s = lo - (pi ? args.p[0].n_seg : 0);
-      r0 = P.seg_offsets[s];
-      len = P.seg_offsets[s + 1] - r0;
-      e = P.seg_expert[s];
-    }
-    const int mt = (len + 15) / 16;
-    const int local = tile - tiles_l[lo];
-    const int m0 = (local % mt) * 16, n0 = (local / mt) * NCOLS;
-    const int K = P.K, N = P.N, nslab = K / 128;
-    const uint8_t* Bb = P.B + (size_t)e * P.b_rows * (K / 2);
-    const uint8_t* Sb = P.b_e8 + (size_t)e * P.b_rows * (K / 32);
-    uint32_t brow[TN];
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-      brow[j] = (MODE == 0 && j >= TN / 2 ? P.up_off + n0 + (j - TN / 2) * 16 : n0 + j * 16) + r;
-    const bool a_ok = m0 + r < len;
-    const int ar = r0 + min(m0 + r, len - 1);
-    const uint32_t arow = P.a_rows ? P.a_rows[ar] : ar;
-
+  const int G = gridDim.x;
+  for (int t0 = xcd_logical(blockIdx.x, G) * NT; t0 < total; t0 += G * NT) {
+    const int tile = t0 + wv / KS;
+    const bool live = tile < total;      // (all true but in the last workgroup)
+    int r0 = 0, len = 0, m0 = 0, n0 = 0, pi = 0;
     f32x4 acc[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    MxUnit<AF4, TN, SL> cur, nxt;
-    int sl = wv * SL;
-    mx_load_a(cur, P, a_ok, arow, sl, nslab, q);
-    mx_load_w(cur, Bb, Sb, brow, K, sl, nslab, q);
-    while (sl < nslab) {
-      sl += 4 * SL;
-      mx_load_a(nxt, P, a_ok, arow, sl, nslab, q);
-      mx_load_w(nxt, Bb, Sb, brow, K, sl, nslab, q);
-      mx_unit_mma(cur, acc, q);
-      cur = nxt;
+    if (live) {
+      int lo = 0, hi = nst - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (tiles_l[mid] <= tile) lo = mid; else hi = mid - 1;
+      }
+      lo = __builtin_amdgcn_readfirstlane(lo);
+      pi = lo < args.p[0].n_seg ? 0 : 1;
+      const MxProblem& P = args.p[pi];
+      int e = 0;
+      len = P.rows;
+      if (P.seg_offsets) {
+        const int s = lo - (pi ? args.p[0].n_seg : 0);
+        r0 = P.seg_offsets[s];
+        len = P.seg_offsets[s + 1] - r0;
+        e = P.seg_expert[s];
+      }
+      const int mt = (len + 15) / 16;
+      const int local = tile - __builtin_amdgcn_readfirstlane(tiles_l[lo]);
+      m0 = (local % mt) * 16;
+      n0 = (local / mt) * NCOLS;
+      const int K = P.K, nslab = K / 128;
+      // this wave's stages: [st0, st0 + ns)
+      const int nst_k = (nslab + 1) / 2, per = (nst_k + KS - 1) / KS;
+      const int st0 = ks * per, ns = min(per, nst_k - st0);
+      MxSrc src;
+      const int64_t e_row = (int64_t)e * P.b_rows;
+      const uint32_t brow_b = K / 2, srow_b = K / 32, arow_b = AF4 ? K / 2 : K * 2;
+      src.rb = buffer_rsrc(P.B + e_row * brow_b, (uint32_t)(P.b_rows * brow_b));
+      src.rs = buffer_rsrc(P.b_e8 + e_row * srow_b, (uint32_t)(P.b_rows * srow_b));
+      src.w = (uint32_t)(n0 + lane / 8) * brow_b + (lane % 8) * 16 + st0 * 128;
+      src.w8 = 8 * brow_b;
+      src.up = P.up_off * brow_b;
+      // two lanes a row, 16 bytes each
+      const int srow = lane / 2;
+      src.ws = (uint32_t)(n0 + (MODE == 0 && srow >= 8 * TN ? P.up_off + srow - 8 * TN : srow)) *
+                   srow_b + (lane % 2) * 16 + st0 * 8;
+      src.ws_up = (MODE == 0 ? P.up_off : 32) * srow_b;
+      // a row past the segment takes an offset beyond the buffer (zeros, and no
+      // traffic; where a buffer ends within a row of 2^32 bytes it reads a
+      // row of it instead: such a row's products are dropped either way)
+      const bool a_ok = m0 + r < len;
+      const int ar = r0 + min(m0 + r, len - 1);
+      const uint32_t arow = P.a_rows ? P.a_rows[ar] : ar;
+      src.ra = buffer_rsrc(P.A, (uint32_t)((size_t)P.a_ld_rows * arow_b));
+      src.a = a_ok ? arow * arow_b + st0 * (AF4 ? 128 : 512) + q * (AF4 ? 16 : 64)
+                   : 0xFFFFFF00u - arow_b;
+      src.as = 0;
+      if constexpr (AF4) {
+        src.ras = buffer_rsrc(P.a_e8, (uint32_t)((size_t)P.a_ld_rows * srow_b));
+        src.as = a_ok ? arow * srow_b + st0 * 8 : 0xFFFFFF00u - srow_b;
+      }
+      if (ns > 0) {
+        constexpr int D = kMxDepth;
+        u32x4 w[D][2 * TN], sc[TN / 2];
+        MxActs<AF4> a[D];
+        // (stages past the wave's last repeat it: every load is issued, so that
+        // the compiler knows what is in flight at every wait)
+        auto load = [&](int d, int st) {
+          const int s = min(st, ns - 1);
+          mx_load_w<MODE, TN>(w[d], src, s);
+          mx_load_a(a[d], src, s);
+        };
+        auto load_sc = [&](int st) {
+#pragma unroll
+          for (int i = 0; i < TN / 2; ++i)
+            sc[i] = __builtin_amdgcn_raw_buffer_load_b128(src.rs, src.ws, st * 8 + i * src.ws_up, 0);
+        };
+        u32x4* wl = turn[wv];
+        u32x4* sl = wl + WB_CH;
+        const int wr = lane / 8, wc = lane % 8;
+        auto body = [&](int st, bool more) __attribute__((always_inline)) {
+#pragma unroll
+          for (int i = 0; i < TN / 2; ++i) sl[i * 64 + lane] = sc[i];
+          if (more) load_sc(st + D);
+#pragma unroll
+          for (int d = 0; d < D; ++d) {
+            u32x4* buf = wl + (d & 1) * (16 * TN * 8);
+#pragma unroll
+            for (int i = 0; i < 2 * TN; ++i) {
+              const int row = i * 8 + wr;
+              buf[row * 8 + (wc ^ swz<8>(row))] = w[d][i];
+            }
+            wave_lds_fence();
+            if (more) mx_load_w<MODE, TN>(w[d], src, min(st + D + d, ns - 1));
+            const int left = nslab - (st0 + st + d) * 2;
+            if (st + d < ns)
+              mx_stage_mma<AF4, TN>(buf, reinterpret_cast<const uint32_t*>(sl) + d * 2, a[d],
+                                    left < 2 ? 1 : 2, r, q, acc);
+            if (more) mx_load_a(a[d], src, min(st + D + d, ns - 1));
+            wave_lds_fence();
+          }
+        };
+        load_sc(0);
+#pragma unroll
+        for (int d = 0; d < D; ++d) load(d, d);
+        int st = 0;
+        for (; st + D < ns; st += D) body(st, true);
+        body(st, false);
+      }
     }
 
-    // the waves' partial sums, then the epilogue on wave 0: lane (r, q) holds
-    // rows 4 q .. 4 q + 3 and column r of each 16 x 16 piece
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < TN; ++j) red[wv][j][lane] = acc[j];
-    __syncthreads();
-    if (wv != 0) continue;
+    // the waves' partial sums, then the epilogue on a tile's first wave: lane
+    // (r, q) holds rows 4 q .. 4 q + 3 and column r of each 16 x 16 piece
     f32x4 v[TN];
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      v[j] = acc[j] + red[1][j][lane] + red[2][j][lane] + red[3][j][lane];
+    for (int j = 0; j < TN; ++j) v[j] = acc[j];
+    if constexpr (KS > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < TN; ++j) red[wv][j][lane] = acc[j];
+      __syncthreads();
+      if (ks != 0) continue;
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int w = 1; w < KS; ++w) v[j] += red[wv + w][j][lane];
+    }
+    if (!live) continue;
+    const MxProblem& P = args.p[pi];
+    const int N = P.N;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int row = m0 + q * 4 + i;
@@ -671,12 +751,33 @@ MxArgs cover(MxArgs g, int bm, int ncols, int min_len, int max_len) {
   return g;
 }
 
-template <int MODE, bool AF4, int TN, int SL>
+template <int MODE, bool AF4, int TN, int KS, int WPE>
 void launch_stream(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
-  auto k = mx_stream_kernel<MODE, AF4, TN, SL>;
+  auto k = mx_stream_kernel<MODE, AF4, TN, KS, WPE>;
   const size_t dyn = (size_t)(g.n_seg_total + 1) * sizeof(int);
   k<<<persistent_grid(k, dyn, 2), 256, dyn, s>>>(
       cover(g, 16, 16 * TN / (MODE == 0 ? 2 : 1), min_len, max_len));
+}
+
+// Waves per tile: enough of them to leave each at most 8 stages of K (K = 8192:
+// 4 waves 191 us, 2 waves 206, 1 wave 202; K = 2048: 1 wave 102 us, 2 waves
+// 112, 4 waves 186), and more where the launch has fewer tiles than the
+// chip takes waves.
+template <int MODE, bool AF4, int TN, int WPE>
+void launch_stream_ks(const MxArgs& g, hipStream_t s) {
+  const int64_t ncols = 16 * TN / (MODE == 0 ? 2 : 1);
+  int64_t tiles = 0;
+  int K = 0;
+  for (int p = 0; p < g.n_probs; ++p) {
+    const int64_t segs = g.p[p].n_seg < g.p[p].rows ? g.p[p].n_seg : g.p[p].rows;
+    tiles += segs * (g.p[p].N / ncols);
+    K = g.p[p].K > K ? g.p[p].K : K;
+  }
+  int ks = K > 4096 ? 4 : K > 2048 ? 2 : 1;
+  while (ks < 4 && tiles * ks < (int64_t)device_cu_count() * 4 && K / ks > 512) ks *= 2;
+  if (ks == 4) launch_stream<MODE, AF4, TN, 4, WPE>(g, 1, kAll, s);
+  else if (ks == 2) launch_stream<MODE, AF4, TN, 2, WPE>(g, 1, kAll, s);
+  else launch_stream<MODE, AF4, TN, 1, WPE>(g, 1, kAll, s);
 }
 
 template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
@@ -701,7 +802,11 @@ void launch_ring_fit(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
 template <int MODE, bool AF4>
 void launch_gemm(const MxArgs& g, bool few_rows, int longest, hipStream_t s) {
   if (few_rows) {
-    launch_stream<MODE, AF4, MODE == 0 && AF4 ? 4 : 2, 2>(g, 1, kAll, s);
+    // GEMM 1 with FP4 activations takes 32 gate and 32 up rows, so that a tile
+    // holds whole 1 x 32 blocks of h; the others 32 weight rows (64 measured
+    // 2-4% slower)
+    if constexpr (AF4) launch_stream_ks<MODE, AF4, MODE == 0 ? 4 : 2, MODE == 0 ? 2 : 3>(g, s);
+    else launch_stream_ks<MODE, AF4, 2, 2>(g, s);
     return;
   }
   constexpr int kSmall = 64, kBig = 256;
