@@ -34,12 +34,30 @@ struct MxProblem {
   int64_t b_rows;           // weight rows per expert
 };
 
+// A value that is the same in every lane, said so: what the compiler takes
+// for a lane's own it keeps in vector registers, and a buffer described by
+// such values is read lane by lane in a loop.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
 struct MxArgs {
   MxProblem p[2];
   int32_t n_probs;
   int32_t n_seg_total;
   int32_t tile_bm, tile_ncols, min_len, max_len;   // as GemmArgs
 };
+
+// silu(z) = z / (1 + e^-z) with the hardware's base-2 exponential and
+// reciprocal: e^-z = 2^(h + l), h the rounded product z * -log2 e and l what
+// its rounding and the constant's left out, so that large |z| lose nothing
+// (about 2^-22 in all; h is rounded to bf16 next).  (expf and a division were
+// a quarter of a 256-row FP4 tile's epilogue.)
+__device__ __forceinline__ float silu_fast(float z) {
+  constexpr float c = -1.44269504f, cl = -1.92596299e-8f;
+  const float h = z * c;
+  const float l = fmaf(z, cl, fmaf(z, c, -h));
+  const float e = __builtin_amdgcn_exp2f(h);
+  return z * __builtin_amdgcn_rcpf(1.0f + fmaf(e, l * 0.693147182f, e));
+}
 
 // ---------------------------------------------------------------- streaming tiles
 // Segments of a few rows: the time is that of reading every active expert's
@@ -63,8 +81,10 @@ struct MxArgs {
 // stages (32 bytes a row) at a time and go through LDS too.
 constexpr int kMxDepth = 4;   // stages in flight
 
-// Byte offsets of a lane's operands at the wave's first stage; the stage goes
-// in the scalar offset.
+// Byte offsets of a lane's operands at the wave's first stage.  (The whole
+// offset goes in the vector offset: the scalar one is no part of the buffer's
+// range check, and the last stage of a K that ends inside it reads past the
+// last row.)
 struct MxSrc {
   __amdgpu_buffer_rsrc_t rb, rs, ra, ras;
   uint32_t w, ws, a, as;
@@ -89,16 +109,16 @@ struct MxActs {
 template <bool AF4>
 __device__ __forceinline__ void mx_load_a(MxActs<AF4>& a, const MxSrc& s, int stage) {
   if constexpr (AF4) {
-    a.v[0][0] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a, stage * 128, 0);
-    a.v[1][0] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a + 64, stage * 128, 0);
-    a.s = __builtin_amdgcn_raw_buffer_load_b64(s.ras, s.as, stage * 8, 0);
+    a.v[0][0] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a + stage * 128, 0, 0);
+    a.v[1][0] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a + stage * 128 + 64, 0, 0);
+    a.s = __builtin_amdgcn_raw_buffer_load_b64(s.ras, s.as + stage * 8, 0, 0);
   } else {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        a.v[i][j] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a + i * 256 + j * 16,
-                                                          stage * 512, 0);
+        a.v[i][j] = __builtin_amdgcn_raw_buffer_load_b128(s.ra, s.a + stage * 512 + i * 256 + j * 16,
+                                                          0, 0);
   }
 }
 
@@ -108,7 +128,7 @@ __device__ __forceinline__ void mx_load_w(u32x4 (&w)[2 * TN], const MxSrc& s, in
   for (int i = 0; i < 2 * TN; ++i) {
     const bool up = MODE == 0 && i >= TN;
     w[i] = __builtin_amdgcn_raw_buffer_load_b128(
-        s.rb, s.w, stage * 128 + (up ? s.up + (i - TN) * s.w8 : i * s.w8), kAuxNT);
+        s.rb, s.w + (stage * 128 + (up ? s.up + (i - TN) * s.w8 : i * s.w8)), 0, kAuxNT);
   }
 }
 
@@ -158,7 +178,7 @@ void mx_stream_kernel(MxArgs args) {
   __shared__ int wsum[256 / 64 + 1];
   extern __shared__ int tiles_l[];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wv = uniform(tid >> 6);
   const int nst = args.n_seg_total;
   build_tile_table<256>(args, tiles_l, wsum, args.tile_bm, args.tile_ncols, args.min_len,
                         args.max_len);
@@ -180,19 +200,19 @@ void mx_stream_kernel(MxArgs args) {
         const int mid = (lo + hi + 1) >> 1;
         if (tiles_l[mid] <= tile) lo = mid; else hi = mid - 1;
       }
-      lo = __builtin_amdgcn_readfirstlane(lo);
+      lo = uniform(lo);
       pi = lo < args.p[0].n_seg ? 0 : 1;
       const MxProblem& P = args.p[pi];
       int e = 0;
       len = P.rows;
       if (P.seg_offsets) {
         const int s = lo - (pi ? args.p[0].n_seg : 0);
-        r0 = P.seg_offsets[s];
-        len = P.seg_offsets[s + 1] - r0;
-        e = P.seg_expert[s];
+        r0 = uniform(P.seg_offsets[s]);
+        len = uniform(P.seg_offsets[s + 1]) - r0;
+        e = uniform(P.seg_expert[s]);
       }
       const int mt = (len + 15) / 16;
-      const int local = tile - __builtin_amdgcn_readfirstlane(tiles_l[lo]);
+      const int local = tile - uniform(tiles_l[lo]);
       m0 = (local % mt) * 16;
       n0 = (local / mt) * NCOLS;
       const int K = P.K, nslab = K / 128;
@@ -240,7 +260,8 @@ void mx_stream_kernel(MxArgs args) {
         auto load_sc = [&](int st) {
 #pragma unroll
           for (int i = 0; i < TN / 2; ++i)
-            sc[i] = __builtin_amdgcn_raw_buffer_load_b128(src.rs, src.ws, st * 8 + i * src.ws_up, 0);
+            sc[i] =
+                __builtin_amdgcn_raw_buffer_load_b128(src.rs, src.ws + (st * 8 + i * src.ws_up), 0, 0);
         };
         u32x4* wl = turn[wv];
         u32x4* sl = wl + WB_CH;
@@ -300,8 +321,8 @@ void mx_stream_kernel(MxArgs args) {
       const int row = m0 + q * 4 + i;
       if constexpr (MODE == 0 && AF4) {
         // h in bf16, then its 1 x 32 block (two columns a lane) as codes
-        const float h0 = __uint_as_float((uint32_t)to_bf16(silu(v[0][i]) * v[2][i]) << 16);
-        const float h1 = __uint_as_float((uint32_t)to_bf16(silu(v[1][i]) * v[3][i]) << 16);
+        const float h0 = __uint_as_float((uint32_t)to_bf16(silu_fast(v[0][i]) * v[2][i]) << 16);
+        const float h1 = __uint_as_float((uint32_t)to_bf16(silu_fast(v[1][i]) * v[3][i]) << 16);
         uint32_t a = max(__float_as_uint(h0) & 0x7fffffffu, __float_as_uint(h1) & 0x7fffffffu);
         a = max(a, (uint32_t)wave_dev::dpp<0xB1>((int)a));
         a = max(a, (uint32_t)wave_dev::dpp<0x4E>((int)a));
@@ -326,7 +347,7 @@ void mx_stream_kernel(MxArgs args) {
 #pragma unroll
           for (int j = 0; j < TN / 2; ++j)
             P.C[(size_t)(r0 + row) * N + n0 + j * 16 + r] =
-                to_bf16(silu(v[j][i]) * v[j + TN / 2][i]);
+                to_bf16(silu_fast(v[j][i]) * v[j + TN / 2][i]);
         }
       } else {
         if (row < len) {
@@ -349,80 +370,90 @@ void mx_stream_kernel(MxArgs args) {
 //
 // A stage holds, per row, 128 bytes of codes (256 elements) with FP4
 // activations, and 256 bytes of bf16 / 64 bytes of codes (128 elements) with
-// bf16 ones, in 16-byte chunks XOR-swizzled by row; then the rows' E8M0
-// bytes, as they are, in 4-byte copies.
+// bf16 ones, in 16-byte chunks XOR-swizzled by row.  (Stages half as deep and
+// twice as many were 15-20% slower: a 64-byte piece costs a request as a whole
+// line does.)  The rows' E8M0 bytes come 16 at a time, those of 512 elements,
+// into two slots of their own behind the ring: a 4- or 8-byte piece per stage
+// cost as many requests as the codes (measured: 10-20% of a launch).
 //
 // FP4 activations: two 16x16x128 FP4 matrix steps a stage.  Lane (r, q)
 // supplies chunk 4 s + q of row r (32 elements, one scale block) and byte
-// 4 s + q of its scales.
+// 4 s + q of the stage's scales.
 // bf16 activations: lane (r, q) reads chunk q of weight row r, 32 codes and
 // one scale, and feeds them to four 16x16x32 steps, 8 at a time, against
 // chunk 4 q + m of the activation row in step m.
-template <bool AF4, int BM, int STAGES, int WAVES_M>
+//
+// Tiles are chained: when a tile's K loop is done, the copies of the next
+// tile's first stages are issued before the output is formed, which is staged
+// in the one ring slot they leave free.
+template <bool AF4, int BM, int STAGES_, int WM_>
 struct MxRing {
-  static constexpr int BN = 256, NTHR = 512, NI = 4;
+  static constexpr int WAVES_M = WM_, BN = 256, NTHR = 512, NI = 4, STAGES = STAGES_;
   static constexpr int BK = AF4 ? 256 : 128;              // elements of a stage
   static constexpr int KCA = AF4 ? 8 : 16, KCB = AF4 ? 8 : 4;   // chunks per row
   static constexpr int RPA = 64 / KCA, RPB = 64 / KCB;    // rows per 1 KiB copy
-  static constexpr int SD = BK / 128;                     // scale dwords per row
-  static constexpr int SRP = 64 / SD;                     // rows per scale copy
-  static constexpr int A_CH = BM * KCA, B_CH = BN * KCB;
-  static constexpr int AS_DW = AF4 ? BM * SD : 0, BS_DW = BN * SD;
-  // 16-byte chunks of a stage, scales included
-  static constexpr int STAGE_CH = A_CH + B_CH + (AS_DW + BS_DW) / 4;
-  static constexpr int RING_CH = STAGES * STAGE_CH;
+  static constexpr int A_CH = BM * KCA, B_CH = BN * KCB, STAGE_CH = A_CH + B_CH;
+  static constexpr int SG = 512 / BK;                     // stages of a scale group
+  static constexpr int AS_CH = AF4 ? BM : 0;              // chunks of a scale slot: one a row
+  static constexpr int SLOT_CH = AS_CH + BN;
+  static constexpr int RING_CH = STAGES * STAGE_CH;       // the scale slots follow
+  static constexpr int LDS_CH = RING_CH + 2 * SLOT_CH;
   static constexpr int A_IT = BM / RPA / NI, B_IT = BN / RPB / NI;
-  static constexpr int S_N = (AS_DW + BS_DW) / 64;        // scale copies of a stage
-  static constexpr int AS_N = AS_DW / 64;                 //   of them activations'
-  static constexpr int S_IT = (S_N + NI - 1) / NI;
-  static constexpr int LPI = A_IT + B_IT + S_IT;          // copies per issuing wave
+  static constexpr int LPI = A_IT + B_IT;                 // copies per issuing wave and stage
+  static constexpr int S_IT = AF4 ? 2 : 1;                //   and per scale group
   static constexpr int WAVES_N = 8 / WAVES_M;
   static constexpr int WM = BM / WAVES_M, WN = BN / WAVES_N;
   static constexpr int TM = WM / 16, TN = WN / 16;
   // weights that no other row tile reads again stream past the caches, where
   // a row's piece is a whole 128-byte line
-  static constexpr int B_AUX = (AF4 && BM < 256) ? kAuxNT : 0;
+  static constexpr int B_AUX = (KCB == 8 && BM < 256) ? kAuxNT : 0;
   static_assert((BM / RPA) % NI == 0 && (BN / RPB) % NI == 0, "copy blocks per wave");
-  static_assert(LPI * (STAGES - 2) < 64, "vmcnt range");
+  static_assert(STAGES == 2 || STAGES == 3, "stage waits");
 };
 
+// Where a tile sits and this lane's copy sources (byte offsets at k = 0; the
+// weight copies of a wave lie at uniform distances).
 template <typename R>
 struct MxTile {
-  int r0, len, e, m0, n0;
+  // (the problem by its number: a pointer into the kernel's arguments, carried
+  // around the tile loop, had them copied to scratch memory)
+  int pi, K, up_off, r0, len, m0, n0;
   bool stream;
-  const MxProblem* P;
   __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
-  uint32_t voff[R::LPI];
+  uint32_t va[R::A_IT], vb, vsa, vsb;
 };
 
 template <int MODE, bool AF4, typename R, int BM>
 __device__ __forceinline__ void mx_ring_setup(const MxArgs& args, const int* tiles_l, int tile,
                                               MxTile<R>& t) {
   const int lane = threadIdx.x & 63;
-  const int wvs = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wvs = uniform(threadIdx.x >> 6);
   int lo = 0, hi = args.n_seg_total - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (tiles_l[mid] <= tile) lo = mid; else hi = mid - 1;
   }
+  lo = uniform(lo);
   const int pi = lo < args.p[0].n_seg ? 0 : 1;
   const MxProblem& P = args.p[pi];
-  t.P = &P;
+  t.pi = pi;
+  t.K = P.K;
+  t.up_off = P.up_off;
   t.r0 = 0;
   t.len = P.rows;
-  t.e = 0;
+  int e = 0;
   if (P.seg_offsets) {
     const int s = lo - (pi ? args.p[0].n_seg : 0);
-    t.r0 = P.seg_offsets[s];
-    t.len = P.seg_offsets[s + 1] - t.r0;
-    t.e = P.seg_expert[s];
+    t.r0 = uniform(P.seg_offsets[s]);
+    t.len = uniform(P.seg_offsets[s + 1]) - t.r0;
+    e = uniform(P.seg_expert[s]);
   }
   const int mt = (t.len + BM - 1) / BM;
   t.stream = mt == 1;
   constexpr int ncols = MODE == 0 ? R::BN / 2 : R::BN;
   const int K = P.K, N = P.N;
   const int nt = (N + ncols - 1) / ncols;
-  const int local = tile - tiles_l[lo];
+  const int local = tile - uniform(tiles_l[lo]);
   const int grp = local / (kGroupM * nt);
   const int first_m = grp * kGroupM;
   const int gm = min(kGroupM, mt - first_m);
@@ -430,7 +461,9 @@ __device__ __forceinline__ void mx_ring_setup(const MxArgs& args, const int* til
   t.m0 = (first_m + lg % gm) * BM;
   t.n0 = (lg / gm) * ncols;
   const uint32_t arow_b = AF4 ? K / 2 : K * 2, brow_b = K / 2, srow_b = K / 32;
-  const int64_t e_row = (int64_t)t.e * P.b_rows;
+  const int64_t e_row = (int64_t)e * P.b_rows;
+  // (weight rows past the expert's last -- the last column tile of a GEMM 2
+  // whose N is an odd multiple of 128 -- lie past the buffers: zeros)
   t.ra = buffer_rsrc(P.A, (uint32_t)((size_t)P.a_ld_rows * arow_b));
   t.rb = buffer_rsrc(P.B + e_row * brow_b, (uint32_t)((size_t)P.b_rows * brow_b));
   if constexpr (AF4) t.rsa = buffer_rsrc(P.a_e8, (uint32_t)((size_t)P.a_ld_rows * srow_b));
@@ -440,233 +473,323 @@ __device__ __forceinline__ void mx_ring_setup(const MxArgs& args, const int* til
     const int ar = t.r0 + min(t.m0 + row, t.len - 1);
     return P.a_rows ? P.a_rows[ar] : ar;
   };
-  auto b_src = [&](int br) -> uint32_t {
-    if (MODE == 0) {
-      const int col = min(t.n0 + (br % (R::BN / 2)), N - 1);
-      return br < R::BN / 2 ? col : P.up_off + col;
-    }
-    return min(t.n0 + br, N - 1);
-  };
 #pragma unroll
-  for (int i = 0; i < R::LPI; ++i) {
-    if (i < R::A_IT) {
-      const int row = (i * R::NI + wvs) * R::RPA + lane / R::KCA;
-      t.voff[i] = a_src(row) * arow_b + ((lane % R::KCA) ^ swz<R::KCA>(row)) * 16;
-    } else if (i < R::A_IT + R::B_IT) {
-      const int br = ((i - R::A_IT) * R::NI + wvs) * R::RPB + lane / R::KCB;
-      t.voff[i] = b_src(br) * brow_b + ((lane % R::KCB) ^ swz<R::KCB>(br)) * 16;
-    } else {
-      // (a copy past the last repeats it: every wave issues the same number)
-      const int c = min((i - R::A_IT - R::B_IT) * R::NI + wvs, R::S_N - 1);
-      const int row = c * R::SRP + lane / R::SD;
-      t.voff[i] = (row < R::AS_N * R::SRP ? a_src(row) : b_src(row - R::AS_N * R::SRP)) * srow_b +
-                  (lane % R::SD) * 4;
-    }
+  for (int i = 0; i < R::A_IT; ++i) {
+    const int row = (i * R::NI + wvs) * R::RPA + lane / R::KCA;
+    t.va[i] = a_src(row) * arow_b + ((lane % R::KCA) ^ swz<R::KCA>(row)) * 16;
   }
+  const int br = wvs * R::RPB + lane / R::KCB;
+  t.vb = (uint32_t)(t.n0 + br) * brow_b + ((lane % R::KCB) ^ swz<R::KCB>(br)) * 16;
+  // scales: a lane a row, 64 rows a copy (a wave past the activation rows
+  // repeats the last 64: every wave issues as many copies)
+  t.vsa = 0;
+  if constexpr (AF4) t.vsa = a_src(min(wvs, BM / 64 - 1) * 64 + lane) * srow_b;
+  const int sr = wvs * 64 + lane;
+  t.vsb = (uint32_t)(t.n0 + (MODE == 0 && sr >= R::BN / 2 ? P.up_off + sr - R::BN / 2 : sr)) * srow_b;
 }
 
-// This wave's copies of K stage kt.  (A last stage that reaches past K reads
-// on into the next row, or zeros past the buffer: those elements enter no
-// product.)
-template <bool AF4, typename R, int STAGES, int AUX>
+// This wave's copies of K stage kt, the scales of a new group of stages first.
+// (A last stage or group that reaches past K reads on into the next row, or
+// zeros past the buffer: those elements enter no product.  The whole offset
+// goes in the vector offset, which the buffer's range check covers; the scalar
+// one is no part of it.)
+template <int MODE, bool AF4, typename R, int BM, int AUX>
 __device__ __forceinline__ void mx_ring_issue(const MxTile<R>& t, u32x4* ring, int kt, int wv) {
-  u32x4* slot = ring + (kt % STAGES) * R::STAGE_CH;
+  if (kt % R::SG == 0) {
+    const int g = kt / R::SG;
+    u32x4* slot = ring + R::RING_CH + (g & 1) * R::SLOT_CH;
+    if constexpr (AF4)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(t.rsa, MOE_LDS_PTR(slot + min(wv, BM / 64 - 1) * 64),
+                                               16, t.vsa + g * 16, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(t.rsb, MOE_LDS_PTR(slot + R::AS_CH + wv * 64), 16,
+                                             t.vsb + g * 16, 0, 0, 0);
+  }
+  u32x4* slot = ring + (kt % R::STAGES) * R::STAGE_CH;
 #pragma unroll
-  for (int i = 0; i < R::LPI; ++i) {
-    if (i < R::A_IT) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(t.ra, MOE_LDS_PTR(slot + (i * R::NI + wv) * 64), 16,
-                                               t.voff[i], kt * (R::KCA * 16), 0, 0);
-    } else if (i < R::A_IT + R::B_IT) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(
-          t.rb, MOE_LDS_PTR(slot + R::A_CH + ((i - R::A_IT) * R::NI + wv) * 64), 16, t.voff[i],
-          kt * (R::KCB * 16), 0, AUX);
-    } else {
-      const int c = min((i - R::A_IT - R::B_IT) * R::NI + wv, R::S_N - 1);
-      u32x4* dst = slot + R::A_CH + R::B_CH + c * 16;
-      if (AF4 && (R::AS_N % R::NI == 0 ? (i - R::A_IT - R::B_IT) * R::NI < R::AS_N : c < R::AS_N))
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(t.rsa, MOE_LDS_PTR(dst), 4, t.voff[i],
-                                                 kt * (R::SD * 4), 0, 0);
-      else
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(t.rsb, MOE_LDS_PTR(dst), 4, t.voff[i],
-                                                 kt * (R::SD * 4), 0, 0);
-    }
+  for (int i = 0; i < R::A_IT; ++i)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(t.ra, MOE_LDS_PTR(slot + (i * R::NI + wv) * 64), 16,
+                                             t.va[i] + kt * (R::KCA * 16), 0, 0, 0);
+  const uint32_t brow_b = t.K / 2;
+#pragma unroll
+  for (int i = 0; i < R::B_IT; ++i) {
+    // weight rows i NI RPB further (GEMM 1: the second half are up rows)
+    constexpr int RPI = R::NI * R::RPB, HALF = R::BN / 2 / RPI;
+    const uint32_t rows = MODE == 0 && i >= HALF ? t.up_off + (i - HALF) * RPI : i * RPI;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        t.rb, MOE_LDS_PTR(slot + R::A_CH + (i * R::NI + wv) * 64), 16,
+        t.vb + (rows * brow_b + kt * (R::KCB * 16)), 0, 0, AUX);
   }
 }
 
-template <bool AF4, typename R, int STAGES>
+template <int MODE, bool AF4, typename R, int BM>
 __device__ __forceinline__ void mx_ring_stage(const MxTile<R>& t, u32x4* ring, int kt, int wv) {
-  if (R::B_AUX && t.stream) mx_ring_issue<AF4, R, STAGES, R::B_AUX>(t, ring, kt, wv);
-  else mx_ring_issue<AF4, R, STAGES, 0>(t, ring, kt, wv);
+  if (R::B_AUX && t.stream) mx_ring_issue<MODE, AF4, R, BM, R::B_AUX>(t, ring, kt, wv);
+  else mx_ring_issue<MODE, AF4, R, BM, 0>(t, ring, kt, wv);
+}
+
+// The first stages of a tile (issuing waves).
+template <int MODE, bool AF4, typename R, int BM>
+__device__ __forceinline__ void mx_ring_prologue(const MxTile<R>& t, u32x4* ring, int wv) {
+  const int KT = (t.K + R::BK - 1) / R::BK;
+  mx_ring_stage<MODE, AF4, R, BM>(t, ring, 0, wv);
+  if (R::STAGES > 2 && KT > 1) mx_ring_stage<MODE, AF4, R, BM>(t, ring, 1, wv);
+}
+
+// Waits until stage kt of KT has landed: at most the copies of the stage
+// after it (three stages) may be outstanding.
+template <typename R>
+__device__ __forceinline__ void mx_ring_wait(int kt, int KT) {
+  if constexpr (R::STAGES == 2) {
+    wait_vmcnt<0>();
+  } else {
+    if (kt + 1 >= KT) wait_vmcnt<0>();
+    else if ((kt + 1) % R::SG == 0) wait_vmcnt<R::LPI + R::S_IT>();
+    else wait_vmcnt<R::LPI>();
+  }
 }
 
 __device__ __forceinline__ i32x8 fp4_operand(u32x4 v) {
   return i32x8{(int)v[0], (int)v[1], (int)v[2], (int)v[3], 0, 0, 0, 0};
 }
 
-// One stage's matrix products.  `half`: only the stage's first 128 elements
-// lie inside K (FP4 activations).
-// (Fragment rows are r plus multiples of 16, so the swizzle is r's, and the
-// fragments of a wave lie at constant distances.)
-template <int MODE, bool AF4, typename R>
-__device__ __forceinline__ void mx_ring_mma(const u32x4* slot, int wm, int wn, int lane, bool half,
+// One stage's matrix products over the wave's first NM row fragments (the
+// rest lie past the segment) and, with FP4 activations, the stage's first NS
+// matrix steps (1 where K ends in the middle of it).
+//
+// A wave's fragment mi covers rows (mi WAVES_M + wm) 16 .. +15 of the tile, so
+// that the live fragments of a partial tile are spread evenly over the
+// waves.  Fragment rows are r plus multiples of 16: the swizzle is r's, and a
+// wave's fragments lie at constant distances.  Operand reads are placed
+// among the products of the fragments before them: two weight fragments
+// ahead, the next step's activation fragments over the last products of the
+// step before.
+template <int MODE, bool AF4, typename R, int NM, int NS>
+__device__ __forceinline__ void mx_ring_mma(const u32x4* ring, int kt, int wm, int wn, int lane,
                                             f32x4 (&acc)[R::TM][R::TN]) {
-  constexpr int TM = R::TM, TN = R::TN;
+  constexpr int TN = R::TN;
+  const u32x4* slot = ring + (kt % R::STAGES) * R::STAGE_CH;
   const int r = lane & 15, q = lane >> 4;
-  const int arow = wm * R::WM + r;
+  const int arow = wm * 16 + r;
   const int brow = wn * (MODE == 0 ? R::WN / 2 : R::WN) + r;
+  constexpr int AF = R::WAVES_M * 16;   // tile rows between a wave's fragments
   // weight rows of fragment ni from brow
   auto b_at = [](int ni) constexpr {
     return MODE == 1 || ni < TN / 2 ? ni * 16 : R::BN / 2 + (ni - TN / 2) * 16;
   };
   const u32x4* As = slot + arow * R::KCA;
   const u32x4* Bs = slot + R::A_CH + brow * R::KCB;
-  const uint32_t* sc = reinterpret_cast<const uint32_t*>(slot + R::A_CH + R::B_CH);
+  const u32x4* sc = ring + R::RING_CH + ((kt / R::SG) & 1) * R::SLOT_CH;
   if constexpr (AF4) {
-    const u32x2* sa2 = reinterpret_cast<const u32x2*>(sc);
-    const u32x2* sb2 = reinterpret_cast<const u32x2*>(sc + R::AS_DW);
-    // bytes q and 4 + q of a row's eight
+    // the stage's 8 scale bytes of a row; q and 4 + q are this lane's
+    const u32x2* sa2 = reinterpret_cast<const u32x2*>(sc + arow) + (kt & 1);
+    const u32x2* sb2 = reinterpret_cast<const u32x2*>(sc + R::AS_CH + brow) + (kt & 1);
     const uint32_t sel = (uint32_t)q | (uint32_t)(4 + q) << 8;
-    int sa[TM], sb[TN];
+    auto scales = [&](const u32x2* at) -> int {
+      const u32x2 v = *at;
+      return (int)__builtin_amdgcn_perm(v.y, v.x, sel);
+    };
+    int sa[NM], sb[TN];
+    u32x4 a[2][NM], b[3];
+    auto load_a = [&](int s, int mi) {
+      a[s][mi] = As[mi * AF * R::KCA + ((s * 4 + q) ^ swz<R::KCA>(r))];
+    };
+    auto load_b = [&](int x) {
+      b[x % 3] = Bs[b_at(x % TN) * R::KCB + (((x / TN) * 4 + q) ^ swz<R::KCB>(r))];
+    };
 #pragma unroll
-    for (int mi = 0; mi < TM; ++mi) {
-      const u32x2 v = sa2[arow + mi * 16];
-      sa[mi] = (int)__builtin_amdgcn_perm(v.y, v.x, sel);
-    }
+    for (int mi = 0; mi < NM; ++mi) sa[mi] = scales(sa2 + mi * AF * 2);
 #pragma unroll
-    for (int ni = 0; ni < TN; ++ni) {
-      const u32x2 v = sb2[brow + b_at(ni)];
-      sb[ni] = (int)__builtin_amdgcn_perm(v.y, v.x, sel);
-    }
+    for (int ni = 0; ni < TN; ++ni) sb[ni] = scales(sb2 + b_at(ni) * 2);
 #pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      if (s == 1 && half) break;
-      i32x8 af[TM], bq[TN];
+    for (int mi = 0; mi < NM; ++mi) load_a(0, mi);
+    load_b(0);
+    load_b(1);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int mi = 0; mi < TM; ++mi)
-        af[mi] = fp4_operand(As[mi * 16 * R::KCA + ((s * 4 + q) ^ swz<R::KCA>(r))]);
+    for (int x = 0; x < NS * TN; ++x) {
+      const int s = x / TN, ni = x % TN;
+      if (x + 2 < NS * TN) load_b(x + 2);
+      if (s == 0 && NS == 2) {
+        // the NM activation fragments of the second step, over the last products
 #pragma unroll
-      for (int ni = 0; ni < TN; ++ni)
-        bq[ni] = fp4_operand(Bs[b_at(ni) * R::KCB + ((s * 4 + q) ^ swz<R::KCB>(r))]);
+        for (int mi = 0; mi < NM; ++mi)
+          if (TN - 1 - mi * TN / NM == ni) load_a(1, mi);
+      }
       // weights as the first operand: lane l gets output row l % 16 and
       // columns 4 (l / 16) .. +3 of each 16 x 16 piece
 #pragma unroll
-      for (int ni = 0; ni < TN; ++ni)
-#pragma unroll
-        for (int mi = 0; mi < TM; ++mi)
-          acc[mi][ni] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                     bq[ni], af[mi], acc[mi][ni], 4, 4, 0, sb[ni], 0, sa[mi])
-                               : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                     bq[ni], af[mi], acc[mi][ni], 4, 4, 1, sb[ni], 1, sa[mi]);
-      // (the second step's operands are not read before the first's are used:
-      // the 256-row tile's accumulators leave no room for both)
+      for (int mi = 0; mi < NM; ++mi)
+        acc[mi][ni] = s == 0 ? __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                   fp4_operand(b[x % 3]), fp4_operand(a[0][mi]), acc[mi][ni], 4, 4,
+                                   0, sb[ni], 0, sa[mi])
+                             : __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                   fp4_operand(b[x % 3]), fp4_operand(a[1][mi]), acc[mi][ni], 4, 4,
+                                   1, sb[ni], 1, sa[mi]);
       __builtin_amdgcn_sched_barrier(0);
     }
   } else {
-    u32x4 bc[TN];
-    float bs[TN];
+    const uint32_t* sb1 = reinterpret_cast<const uint32_t*>(sc + brow) + (kt & 3);
+    u32x4 bc[TN], a[2][NM];
+    uint32_t bs[TN];
+    auto load_a = [&](int m, int mi) {
+      a[m & 1][mi] = As[mi * AF * R::KCA + ((4 * q + m) ^ swz<R::KCA>(r))];
+    };
 #pragma unroll
     for (int ni = 0; ni < TN; ++ni) {
       bc[ni] = Bs[b_at(ni) * R::KCB + (q ^ swz<R::KCB>(r))];
-      bs[ni] = e8m0_float((sc[brow + b_at(ni)] >> (8 * q)) & 0xffu);
+      bs[ni] = sb1[b_at(ni) * 4];
     }
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      bf16x8 af[TM], bq[TN];
+    for (int mi = 0; mi < NM; ++mi) load_a(0, mi);
+    float bf[TN];
 #pragma unroll
-      for (int mi = 0; mi < TM; ++mi)
-        af[mi] = __builtin_bit_cast(bf16x8,
-                                    As[mi * 16 * R::KCA + ((4 * q + m) ^ swz<R::KCA>(r))]);
+    for (int ni = 0; ni < TN; ++ni) bf[ni] = e8m0_float((bs[ni] >> (8 * q)) & 0xffu);
+    u32x4 b = e2m1x8_to_bf16(bc[0][0], bf[0]);
 #pragma unroll
-      for (int ni = 0; ni < TN; ++ni)
-        bq[ni] = __builtin_bit_cast(bf16x8, e2m1x8_to_bf16(bc[ni][m], bs[ni]));
+    for (int x = 0; x < 4 * TN; ++x) {
+      const int m = x / TN, ni = x % TN;
+      if (m < 3) {
 #pragma unroll
-      for (int ni = 0; ni < TN; ++ni)
+        for (int mi = 0; mi < NM; ++mi)
+          if (mi * TN / NM == ni) load_a(m + 1, mi);
+      }
+      u32x4 nb = b;
+      if (x + 1 < 4 * TN)
+        nb = e2m1x8_to_bf16(bc[(x + 1) % TN][(x + 1) / TN], bf[(x + 1) % TN]);
 #pragma unroll
-        for (int mi = 0; mi < TM; ++mi)
-          acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bq[ni], af[mi], acc[mi][ni], 0, 0,
-                                                                0);
+      for (int mi = 0; mi < NM; ++mi)
+        acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            __builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a[m & 1][mi]), acc[mi][ni],
+            0, 0, 0);
+      b = nb;
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
 
-// The tile's output: every wave stages its rows in its own part of the idle
-// ring, chunk c of row rr at c ^ (rr % CPR), and whole 16-byte row chunks go
+// The K loop of one tile over the wave's NM live row fragments (0: copies and
+// barriers only).  (One loop for each NM, chosen outside it: variants inside
+// one loop cost a second set of accumulators where they meet.)
+template <int MODE, bool AF4, typename R, int BM, int NM>
+__device__ __forceinline__ void mx_ring_kloop(const MxTile<R>& t, u32x4* ring, int wm, int wn,
+                                              int wvs, int lane, f32x4 (&acc)[R::TM][R::TN]) {
+  const int K = t.K, KT = (K + R::BK - 1) / R::BK;
+  auto enter = [&](int kt) {
+    if (wvs < R::NI) mx_ring_wait<R>(kt, KT);
+    raw_barrier();
+    if (kt + R::STAGES - 1 < KT && wvs < R::NI)
+      mx_ring_stage<MODE, AF4, R, BM>(t, ring, kt + R::STAGES - 1, wvs);
+  };
+  const int full = K / R::BK;
+  for (int kt = 0; kt < full; ++kt) {
+    enter(kt);
+    if constexpr (NM > 0) mx_ring_mma<MODE, AF4, R, NM, AF4 ? 2 : 1>(ring, kt, wm, wn, lane, acc);
+  }
+  if (AF4 && full < KT) {
+    enter(full);
+    if constexpr (NM > 0) mx_ring_mma<MODE, AF4, R, NM, 1>(ring, full, wm, wn, lane, acc);
+  }
+}
+
+template <int MODE, bool AF4, typename R, int BM, int NM = R::TM>
+__device__ __forceinline__ void mx_ring_kloop_live(const MxTile<R>& t, u32x4* ring, int wm, int wn,
+                                                   int wvs, int lane, int live,
+                                                   f32x4 (&acc)[R::TM][R::TN]) {
+  if constexpr (NM > 0) {
+    if (live < NM)
+      return mx_ring_kloop_live<MODE, AF4, R, BM, NM - 1>(t, ring, wm, wn, wvs, lane, live, acc);
+  }
+  mx_ring_kloop<MODE, AF4, R, BM, NM>(t, ring, wm, wn, wvs, lane, acc);
+}
+
+// The tile's output through the free ring slot: every wave stages its rows in
+// a part of its own, chunk c of row rr at c ^ (rr % CPR), in PASSES column
+// parts where the slot does not hold them all, and whole 16-byte row chunks go
 // out; a chunk past the segment or past N takes an offset beyond the store's
 // range and is dropped.  GEMM 1 with FP4 activations: after a barrier, 16
 // lanes take one row's 128 columns of h, 4 lanes a 1 x 32 block, and write
 // its codes (64 contiguous bytes a row) and scales.
-template <int MODE, bool AF4, typename R>
-__device__ __forceinline__ void mx_ring_store(const MxTile<R>& t, const u32x2* out, u32x4* ring) {
+template <int MODE, bool AF4, typename R, int BM>
+__device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R>& t,
+                                              const u32x2* out, u32x4* slot) {
   constexpr int TM = R::TM, WM = R::WM, NPM = MODE == 0 ? R::TN / 2 : R::TN;
   constexpr int COUT = MODE == 0 ? R::WN / 2 : R::WN;
-  constexpr int CPR = COUT / 8, RPI = 64 / CPR;
+  constexpr int PASSES = BM * (MODE == 0 ? R::BN / 2 : R::BN) / 8 > R::STAGE_CH ? 2 : 1;
+  constexpr int NP = NPM / PASSES, CPR = COUT / PASSES / 8, RPI = 64 / CPR;
   static_assert(CPR <= 16 && 64 % CPR == 0 && WM % RPI == 0, "output transpose shape");
+  static_assert(8 * WM * CPR <= R::STAGE_CH, "the staged output fits a slot");
+  static_assert(!(MODE == 0 && AF4) || PASSES == 1, "h's blocks cross the waves' columns");
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));   // (addresses formed here, not kept through the K loop)
   const int wv = threadIdx.x >> 6;
   const int wm = wv / R::WAVES_N, wn = wv % R::WAVES_N;
-  u32x4* reg = ring + (size_t)wv * WM * CPR;
-#pragma unroll
-  for (int mi = 0; mi < TM; ++mi) {
-    const int rr = mi * 16 + (lane & 15);
-#pragma unroll
-    for (int ni = 0; ni < NPM; ++ni) {
-      const int c = ni * 2 + ((lane >> 4) >> 1);
-      reinterpret_cast<u32x2*>(reg + rr * CPR + (c ^ (rr % CPR)))[(lane >> 4) & 1] =
-          out[mi * NPM + ni];
-    }
-  }
-  const MxProblem& P = *t.P;
+  u32x4* reg = slot + (size_t)wv * WM * CPR;
   const int N = P.N;
-  if constexpr (MODE == 0 && AF4) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    raw_barrier();   // every wave's rows are staged
-    constexpr int BM = WM * (8 / R::WAVES_N);
-    const __amdgpu_buffer_rsrc_t rq =
-        buffer_rsrc(P.Cq + (size_t)t.r0 * (N / 2), (uint32_t)((size_t)t.len * (N / 2)));
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));
-    const int cc = tid & 15;                          // this lane's 8 of the 128 columns
-    const int swn = cc / CPR, sc = cc % CPR;
 #pragma unroll
-    for (int it = 0; it < BM / 32; ++it) {
-      const int row = it * 32 + (tid >> 4);
-      const int swm = row / WM, rr = row % WM;
-      const u32x4 v = ring[(size_t)(swm * R::WAVES_N + swn) * WM * CPR + rr * CPR + (sc ^ (rr % CPR))];
-      float f[8];
-      uint32_t a = 0;
+  for (int p = 0; p < PASSES; ++p) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(v[j] << 16);
-        f[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
-        a = max(a, max(__float_as_uint(f[2 * j]) & 0x7fffffffu,
-                       __float_as_uint(f[2 * j + 1]) & 0x7fffffffu));
+    for (int mi = 0; mi < TM; ++mi) {
+      const int rr = mi * 16 + (lane & 15);   // tile row (mi WAVES_M + wm) 16 + lane % 16
+#pragma unroll
+      for (int ni = 0; ni < NP; ++ni) {
+        const int c = ni * 2 + ((lane >> 4) >> 1);
+        reinterpret_cast<u32x2*>(reg + rr * CPR + (c ^ (rr % CPR)))[(lane >> 4) & 1] =
+            out[mi * NPM + p * NP + ni];
       }
-      a = max(a, (uint32_t)wave_dev::dpp<0xB1>((int)a));
-      a = max(a, (uint32_t)wave_dev::dpp<0x4E>((int)a));
-      const uint32_t b = block_e8m0(a);
-      const uint32_t codes = e2m1x8(f, b);
-      const int grow = t.m0 + row;
-      const uint32_t off = grow < t.len
-                               ? ((uint32_t)grow * (uint32_t)N + (uint32_t)(t.n0 + cc * 8)) / 2u
-                               : 0xFFFFFFF0u;
-      __builtin_amdgcn_raw_buffer_store_b32(codes, rq, off, 0, 0);
-      if ((cc & 3) == 0 && grow < t.len)
-        P.c_e8[(size_t)(t.r0 + grow) * (N / 32) + (t.n0 + cc * 8) / 32] = (uint8_t)b;
     }
-  } else {
-    const __amdgpu_buffer_rsrc_t rc =
-        buffer_rsrc(P.C + (size_t)t.r0 * N, (uint32_t)((size_t)t.len * N * 2));
-    const int col0 = t.n0 + wn * COUT;
+    if constexpr (MODE == 0 && AF4) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      raw_barrier();   // every wave's rows are staged
+      const __amdgpu_buffer_rsrc_t rq =
+          buffer_rsrc(P.Cq + (size_t)t.r0 * (N / 2), (uint32_t)((size_t)t.len * (N / 2)));
+      int tid = threadIdx.x;
+      asm volatile("" : "+v"(tid));
+      const int cc = tid & 15;                          // this lane's 8 of the 128 columns
+      const int swn = cc / CPR, sc = cc % CPR;
 #pragma unroll
-    for (int it = 0; it < WM / RPI; ++it) {
-      const int rr = it * RPI + lane / CPR, c = lane % CPR;
-      const u32x4 v = reg[rr * CPR + (c ^ (rr % CPR))];
-      const int row = t.m0 + wm * WM + rr, col = col0 + c * 8;
-      const uint32_t off = (row < t.len && col < N)
-                               ? ((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u
-                               : 0xFFFFFFF0u;
-      __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, MODE == 1 ? kAuxNT : 0);
+      for (int it = 0; it < BM / 32; ++it) {
+        const int row = it * 32 + (tid >> 4);
+        const int frag = row / 16, swm = frag % R::WAVES_M;
+        const int rr = frag / R::WAVES_M * 16 + row % 16;
+        const u32x4 v =
+            slot[(size_t)(swm * R::WAVES_N + swn) * WM * CPR + rr * CPR + (sc ^ (rr % CPR))];
+        float f[8];
+        uint32_t a = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[2 * j] = __uint_as_float(v[j] << 16);
+          f[2 * j + 1] = __uint_as_float(v[j] & 0xffff0000u);
+          a = max(a, max(__float_as_uint(f[2 * j]) & 0x7fffffffu,
+                         __float_as_uint(f[2 * j + 1]) & 0x7fffffffu));
+        }
+        a = max(a, (uint32_t)wave_dev::dpp<0xB1>((int)a));
+        a = max(a, (uint32_t)wave_dev::dpp<0x4E>((int)a));
+        const uint32_t b = block_e8m0(a);
+        const uint32_t codes = e2m1x8(f, b);
+        const int grow = t.m0 + row;
+        const uint32_t off = grow < t.len
+                                 ? ((uint32_t)grow * (uint32_t)N + (uint32_t)(t.n0 + cc * 8)) / 2u
+                                 : 0xFFFFFFF0u;
+        __builtin_amdgcn_raw_buffer_store_b32(codes, rq, off, 0, 0);
+        if ((cc & 3) == 0 && grow < t.len)
+          P.c_e8[(size_t)(t.r0 + grow) * (N / 32) + (t.n0 + cc * 8) / 32] = (uint8_t)b;
+      }
+    } else {
+      wave_lds_fence();
+      const __amdgpu_buffer_rsrc_t rc =
+          buffer_rsrc(P.C + (size_t)t.r0 * N, (uint32_t)((size_t)t.len * N * 2));
+      const int col0 = t.n0 + wn * COUT + p * (COUT / PASSES);
+#pragma unroll
+      for (int it = 0; it < WM / RPI; ++it) {
+        const int rr = it * RPI + lane / CPR, c = lane % CPR;
+        const u32x4 v = reg[rr * CPR + (c ^ (rr % CPR))];
+        const int row = t.m0 + (rr / 16 * R::WAVES_M + wm) * 16 + rr % 16, col = col0 + c * 8;
+        const uint32_t off = (row < t.len && col < N)
+                                 ? ((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u
+                                 : 0xFFFFFFF0u;
+        __builtin_amdgcn_raw_buffer_store_b128(v, rc, off, 0, MODE == 1 ? kAuxNT : 0);
+      }
+      wave_lds_fence();
     }
   }
 }
@@ -677,25 +800,22 @@ __global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
   constexpr int TM = R::TM, TN = R::TN, NPM = MODE == 0 ? TN / 2 : TN;
   // (the ring and the tile table are the only LDS objects, as in gemm.hip's
   // ring kernel; the table's scan borrows the idle ring)
-  __shared__ __attribute__((aligned(1024))) u32x4 ring[R::RING_CH];
+  __shared__ __attribute__((aligned(1024))) u32x4 ring[R::LDS_CH];
   extern __shared__ int tiles_l[];
   build_tile_table<512>(args, tiles_l, reinterpret_cast<int*>(ring), args.tile_bm,
                         args.tile_ncols, args.min_len, args.max_len);
-  const int total = tiles_l[args.n_seg_total];
+  const int total = uniform(tiles_l[args.n_seg_total]);
   const int lane = threadIdx.x & 63;
-  const int wvs = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wvs = uniform(threadIdx.x >> 6);
   const int wm = wvs / R::WAVES_N, wn = wvs % R::WAVES_N;
   const int G = gridDim.x;
-  for (int tile = xcd_logical(blockIdx.x, G); tile < total; tile += G) {
-    MxTile<R> t;
-    mx_ring_setup<MODE, AF4, R, BM>(args, tiles_l, tile, t);
-    raw_barrier();   // the previous tile's output has left the ring
-    const int K = t.P->K, KT = (K + R::BK - 1) / R::BK;
-    if (wvs < R::NI) {
-#pragma unroll
-      for (int st = 0; st < STAGES - 1; ++st)
-        if (st < KT) mx_ring_stage<AF4, R, STAGES>(t, ring, st, wvs);
-    }
+  int tile = xcd_logical(blockIdx.x, G);
+  if (tile >= total) return;
+  MxTile<R> t;
+  mx_ring_setup<MODE, AF4, R, BM>(args, tiles_l, tile, t);
+  raw_barrier();   // (the table's scan has left the ring)
+  if (wvs < R::NI) mx_ring_prologue<MODE, AF4, R, BM>(t, ring, wvs);
+  for (;;) {
     u32x2 outv[TM * NPM];
     {
       f32x4 acc[TM][TN];
@@ -703,33 +823,26 @@ __global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
       for (int mi = 0; mi < TM; ++mi)
 #pragma unroll
         for (int ni = 0; ni < TN; ++ni) acc[mi][ni] = f32x4{0.f, 0.f, 0.f, 0.f};
-      // a wave whose rows all lie past the segment takes part in the copies
-      // and barriers only
-      const bool rows_here = t.m0 + wm * R::WM < t.len;
-      int kt = 0;
-      do {   // (K >= 128: at least one stage; a loop that may run none held a
-             // second set of output registers, with spills)
-        if (wvs < R::NI) wait_stages<R::LPI, STAGES - 2>(min(STAGES - 2, KT - 1 - kt));
-        raw_barrier();
-        if (kt + STAGES - 1 < KT && wvs < R::NI)
-          mx_ring_stage<AF4, R, STAGES>(t, ring, kt + STAGES - 1, wvs);
-        if (!rows_here) continue;
-        mx_ring_mma<MODE, AF4, R>(ring + (kt % STAGES) * R::STAGE_CH, wm, wn, lane,
-                                  AF4 && kt * R::BK + 128 >= K, acc);
-      } while (++kt < KT);
+      // row fragments of this wave that hold rows of the segment (a wave with
+      // none takes part in the copies and barriers only)
+      const int live =
+          min(TM, ((t.len - t.m0 + 15) / 16 - wm + R::WAVES_M - 1) / R::WAVES_M);
+      mx_ring_kloop_live<MODE, AF4, R, BM>(t, ring, wm, wn, wvs, lane, live, acc);
 #pragma unroll
       for (int mi = 0; mi < TM; ++mi) {
         float rs = 1.0f;
-        if (MODE == 1 && t.P->scale) {
-          const int row = t.m0 + wm * R::WM + mi * 16 + (lane & 15);
-          rs = t.P->scale[t.r0 + min(row, t.len - 1)];
+        const float* scale = args.p[t.pi].scale;
+        if (MODE == 1 && scale) {
+          const int row = t.m0 + (mi * R::WAVES_M + wm) * 16 + (lane & 15);
+          rs = scale[t.r0 + min(row, t.len - 1)];
         }
 #pragma unroll
         for (int ni = 0; ni < NPM; ++ni) {
           if (MODE == 0) {
             const f32x4 g = acc[mi][ni], u = acc[mi][ni + TN / 2];
-            outv[mi * NPM + ni] = u32x2{pack_bf16x2(silu(g[0]) * u[0], silu(g[1]) * u[1]),
-                                        pack_bf16x2(silu(g[2]) * u[2], silu(g[3]) * u[3])};
+            outv[mi * NPM + ni] =
+                u32x2{pack_bf16x2(silu_fast(g[0]) * u[0], silu_fast(g[1]) * u[1]),
+                      pack_bf16x2(silu_fast(g[2]) * u[2], silu_fast(g[3]) * u[3])};
           } else {
             const f32x4 y = acc[mi][ni];
             outv[mi * NPM + ni] =
@@ -738,8 +851,15 @@ __global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
         }
       }
     }
-    raw_barrier();   // every wave is done reading the ring: it takes the output
-    mx_ring_store<MODE, AF4, R>(t, outv, ring);
+    raw_barrier();   // every wave is done reading the ring
+    const MxTile<R> done = t;
+    tile += G;
+    if (tile < total) {
+      mx_ring_setup<MODE, AF4, R, BM>(args, tiles_l, tile, t);
+      if (wvs < R::NI) mx_ring_prologue<MODE, AF4, R, BM>(t, ring, wvs);
+    }
+    mx_ring_store<MODE, AF4, R, BM>(args.p[done.pi], done, outv, ring + (STAGES - 1) * R::STAGE_CH);
+    if (tile >= total) break;
   }
 }
 
@@ -788,13 +908,18 @@ void launch_ring(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
       cover(g, BM, MODE == 0 ? 128 : 256, min_len, max_len));
 }
 
-// A ring launch over the segments of [min_len, max_len) rows, on STAGES
-// stages if the tile table fits beside them, else on two.
-template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
+// The ring and the launch's tile table fit the LDS.
+template <typename R>
+bool ring_fits(const MxArgs& g) {
+  return (size_t)R::LDS_CH * 16 + (size_t)(g.n_seg_total + 1) * sizeof(int) + 64 <= kMaxLdsBytes;
+}
+
+// A ring launch over the segments of [min_len, max_len) rows, on three stages
+// if the tile table fits beside them, else on two.
+template <int MODE, bool AF4, int BM, int WAVES_M>
 void launch_ring_fit(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
-  const size_t ring = (size_t)MxRing<AF4, BM, STAGES, WAVES_M>::RING_CH * 16;
-  if (ring + (size_t)(g.n_seg_total + 1) * sizeof(int) + 64 <= kMaxLdsBytes)
-    launch_ring<MODE, AF4, BM, STAGES, WAVES_M>(g, min_len, max_len, s);
+  if (ring_fits<MxRing<AF4, BM, 3, WAVES_M>>(g))
+    launch_ring<MODE, AF4, BM, 3, WAVES_M>(g, min_len, max_len, s);
   else
     launch_ring<MODE, AF4, BM, 2, WAVES_M>(g, min_len, max_len, s);
 }
@@ -810,12 +935,15 @@ void launch_gemm(const MxArgs& g, bool few_rows, int longest, hipStream_t s) {
     return;
   }
   constexpr int kSmall = 64, kBig = 256;
-  launch_ring_fit<MODE, AF4, 64, 3, 2>(g, 1, kSmall + 1, s);
   if constexpr (AF4) {
-    launch_ring_fit<MODE, AF4, 128, 3, 2>(g, kSmall + 1, kBig, s);
-    if (longest >= kBig) launch_ring_fit<MODE, AF4, 256, 2, 4>(g, kBig, kAll, s);
+    launch_ring_fit<MODE, AF4, 64, 2>(g, 1, kSmall + 1, s);
+    // (the 256-row tile's ring leaves room for the table of about 4000 segments)
+    const bool any_big = longest >= kBig && ring_fits<MxRing<AF4, 256, 2, 4>>(g);
+    launch_ring_fit<MODE, AF4, 128, 2>(g, kSmall + 1, any_big ? kBig : kAll, s);
+    if (any_big) launch_ring<MODE, AF4, 256, 2, 4>(g, kBig, kAll, s);
   } else {
-    launch_ring_fit<MODE, AF4, 128, 3, 2>(g, kSmall + 1, kAll, s);
+    launch_ring_fit<MODE, AF4, 64, 2>(g, 1, kSmall + 1, s);
+    launch_ring_fit<MODE, AF4, 128, 2>(g, kSmall + 1, kAll, s);
   }
 }
 
