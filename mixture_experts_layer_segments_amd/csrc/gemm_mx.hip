@@ -794,22 +794,33 @@ __device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R
   }
 }
 
+constexpr int kMxSmall = 64, kMxBig = 256;
+
+// 16-byte chunks of LDS that the classes of a launch need.
+template <bool AF4, int STAGES, bool BIG>
+constexpr int mx_ring_lds() {
+  constexpr int a = MxRing<AF4, 64, STAGES, 2>::LDS_CH, b = MxRing<AF4, 128, STAGES, 2>::LDS_CH,
+                c = BIG ? MxRing<AF4, 256, 2, 4>::LDS_CH : 0;
+  return a > b ? (a > c ? a : c) : (b > c ? b : c);
+}
+
+// Every tile of one class: the segments of [min_len, max_len) rows on tiles of
+// BM rows.  This workgroup takes tiles first, first + G, ...
 template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
-__global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
+__device__ __forceinline__ void mx_ring_class(const MxArgs& args, u32x4* ring, int* tiles_l,
+                                              int min_len, int max_len, int first) {
   using R = MxRing<AF4, BM, STAGES, WAVES_M>;
   constexpr int TM = R::TM, TN = R::TN, NPM = MODE == 0 ? TN / 2 : TN;
-  // (the ring and the tile table are the only LDS objects, as in gemm.hip's
-  // ring kernel; the table's scan borrows the idle ring)
-  __shared__ __attribute__((aligned(1024))) u32x4 ring[R::LDS_CH];
-  extern __shared__ int tiles_l[];
-  build_tile_table<512>(args, tiles_l, reinterpret_cast<int*>(ring), args.tile_bm,
-                        args.tile_ncols, args.min_len, args.max_len);
+  __syncthreads();   // (the class before has left the LDS)
+  // (the table's scan borrows the idle ring)
+  build_tile_table<512>(args, tiles_l, reinterpret_cast<int*>(ring), BM,
+                        MODE == 0 ? R::BN / 2 : R::BN, min_len, max_len);
   const int total = uniform(tiles_l[args.n_seg_total]);
   const int lane = threadIdx.x & 63;
   const int wvs = uniform(threadIdx.x >> 6);
   const int wm = wvs / R::WAVES_N, wn = wvs % R::WAVES_N;
   const int G = gridDim.x;
-  int tile = xcd_logical(blockIdx.x, G);
+  int tile = first;
   if (tile >= total) return;
   MxTile<R> t;
   mx_ring_setup<MODE, AF4, R, BM>(args, tiles_l, tile, t);
@@ -863,6 +874,39 @@ __global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
   }
 }
 
+// One grouped GEMM over three classes of segments: up to 64 rows (64-row tiles,
+// bound by reading their experts' weights), up to 255 (128-row tiles; with
+// bf16 activations all longer ones too) and, with FP4 activations, 256 and
+// more (256-row tiles, bound by the matrix units).  Every workgroup takes its
+// share of each class, half of them in the opposite order, so that the
+// classes that wait for memory and those that compute run side by side.
+template <int MODE, bool AF4, int STAGES, bool BIG>
+__global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
+  // (the ring and the tile table are the only LDS objects, as in gemm.hip's
+  // ring kernel)
+  __shared__ __attribute__((aligned(1024))) u32x4 ring[mx_ring_lds<AF4, STAGES, BIG>()];
+  extern __shared__ int tiles_l[];
+  const int G = gridDim.x, logical = xcd_logical(blockIdx.x, G);
+  // (the classes' last, partial rounds start at different workgroups)
+  const int second = (logical + G / 3) % G, third = (logical + 2 * (G / 3)) % G;
+  constexpr int n = BIG ? 3 : 2;
+  for (int i = 0; i < n; ++i) {
+    switch (logical & 1 ? i : n - 1 - i) {
+      case 0:
+        mx_ring_class<MODE, AF4, 64, STAGES, 2>(args, ring, tiles_l, 1, kMxSmall + 1, logical);
+        break;
+      case 1:
+        mx_ring_class<MODE, AF4, 128, STAGES, 2>(args, ring, tiles_l, kMxSmall + 1,
+                                                 BIG ? kMxBig : kAll, second);
+        break;
+      default:
+        if constexpr (BIG)
+          mx_ring_class<MODE, AF4, 256, 2, 4>(args, ring, tiles_l, kMxBig, kAll, third);
+        break;
+    }
+  }
+}
+
 MxArgs cover(MxArgs g, int bm, int ncols, int min_len, int max_len) {
   g.tile_bm = bm;
   g.tile_ncols = ncols;
@@ -900,28 +944,15 @@ void launch_stream_ks(const MxArgs& g, hipStream_t s) {
   else launch_stream<MODE, AF4, TN, 1, WPE>(g, 1, kAll, s);
 }
 
-template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
-void launch_ring(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
-  auto k = mx_ring_kernel<MODE, AF4, BM, STAGES, WAVES_M>;
+// Launches the ring kernel if its LDS holds the launch's tile table beside the
+// ring.
+template <int MODE, bool AF4, int STAGES, bool BIG>
+bool launch_ring(const MxArgs& g, hipStream_t s) {
   const size_t dyn = (size_t)(g.n_seg_total + 1) * sizeof(int);
-  k<<<persistent_grid(k, dyn, 1, 512), 512, dyn, s>>>(
-      cover(g, BM, MODE == 0 ? 128 : 256, min_len, max_len));
-}
-
-// The ring and the launch's tile table fit the LDS.
-template <typename R>
-bool ring_fits(const MxArgs& g) {
-  return (size_t)R::LDS_CH * 16 + (size_t)(g.n_seg_total + 1) * sizeof(int) + 64 <= kMaxLdsBytes;
-}
-
-// A ring launch over the segments of [min_len, max_len) rows, on three stages
-// if the tile table fits beside them, else on two.
-template <int MODE, bool AF4, int BM, int WAVES_M>
-void launch_ring_fit(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
-  if (ring_fits<MxRing<AF4, BM, 3, WAVES_M>>(g))
-    launch_ring<MODE, AF4, BM, 3, WAVES_M>(g, min_len, max_len, s);
-  else
-    launch_ring<MODE, AF4, BM, 2, WAVES_M>(g, min_len, max_len, s);
+  if ((size_t)mx_ring_lds<AF4, STAGES, BIG>() * 16 + dyn + 64 > kMaxLdsBytes) return false;
+  auto k = mx_ring_kernel<MODE, AF4, STAGES, BIG>;
+  k<<<persistent_grid(k, dyn, 1, 512), 512, dyn, s>>>(g);
+  return true;
 }
 
 template <int MODE, bool AF4>
@@ -934,17 +965,11 @@ void launch_gemm(const MxArgs& g, bool few_rows, int longest, hipStream_t s) {
     else launch_stream_ks<MODE, AF4, 2, 2>(g, s);
     return;
   }
-  constexpr int kSmall = 64, kBig = 256;
-  if constexpr (AF4) {
-    launch_ring_fit<MODE, AF4, 64, 2>(g, 1, kSmall + 1, s);
-    // (the 256-row tile's ring leaves room for the table of about 4000 segments)
-    const bool any_big = longest >= kBig && ring_fits<MxRing<AF4, 256, 2, 4>>(g);
-    launch_ring_fit<MODE, AF4, 128, 2>(g, kSmall + 1, any_big ? kBig : kAll, s);
-    if (any_big) launch_ring<MODE, AF4, 256, 2, 4>(g, kBig, kAll, s);
-  } else {
-    launch_ring_fit<MODE, AF4, 64, 2>(g, 1, kSmall + 1, s);
-    launch_ring_fit<MODE, AF4, 128, 2>(g, kSmall + 1, kAll, s);
-  }
+  // (256-row tiles with FP4 activations only: with bf16 ones 128-row tiles are
+  // bound by the matrix units already)
+  const bool big = AF4 && longest >= kMxBig;
+  if (big && (launch_ring<MODE, AF4, 3, AF4>(g, s) || launch_ring<MODE, AF4, 2, AF4>(g, s))) return;
+  if (!launch_ring<MODE, AF4, 3, false>(g, s)) launch_ring<MODE, AF4, 2, false>(g, s);
 }
 
 }  // namespace
