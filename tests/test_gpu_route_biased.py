@@ -112,12 +112,64 @@ def test_saturated_and_extreme_logits(moe):
     _check(moe, cfg.replace(score="softmax", renormalize=0), lg, None, ties=True)
 
 
+@pytest.mark.parametrize("name", ["softmax-E7k3g1", "sigmoid-E128k8g1", "softmax-E128k8g1",
+                                  "sigmoid-E256k8g8", "softmax-E256k8g8", "softmax-E512k6g16",
+                                  "sigmoid-E200k32g1", "softmax-E16k4g16"])
+@pytest.mark.parametrize("step", [1, 16, 256])
+def test_near_ties(moe, name, step):
+    """Logits a few fp32 steps apart, among the picked and at the cut, in some
+    tokens of a wave and not in others: no fp32 score tells them apart, the
+    64-bit ones do."""
+    cfg = CASES[name].replace(T=64)
+    rng = np.random.default_rng(step)
+    lg = rng.standard_normal((cfg.T, cfg.E)).astype(np.float32)
+    lg[rng.random(lg.shape) < 0.05] = -np.inf
+    for t in range(0, cfg.T, 3):
+        v = np.float32(rng.uniform(0.5, 2.5))
+        at = rng.choice(cfg.E, max(2, cfg.E // 3), replace=False)
+        near = (v.view(np.int32) + step * rng.permutation(at.size)).astype(np.int32)
+        lg[t, at] = near.view(np.float32)
+    _check(moe, cfg, lg, None)
+    # a large bias of one value: the sums tell them apart less, the order stays
+    _check(moe, cfg, lg, np.full(cfg.E, 0.75, np.float32), 2.5)
+
+
+def test_biases_of_both_signs_cancel_in_group_scores(moe):
+    """Group scores near zero from large members: what a sum in fp32 loses is
+    no order."""
+    for score in ("softmax", "sigmoid"):
+        cfg = mi.MoEShape("r", T=100, H=128, E=64, k=4, I=128, score=score, n_group=8,
+                          topk_group=3, group_score_topn=8)
+        rng = np.random.default_rng(12)
+        lg = rng.standard_normal((cfg.T, 64)).astype(np.float32)
+        half = rng.uniform(50, 100, 32).astype(np.float32)
+        bias = np.empty(64, np.float32)
+        bias[0::2], bias[1::2] = half, -half
+        _check(moe, cfg, lg, bias)
+
+
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 1000, 4097])
 def test_batch_sizes(moe, T):
     cfg = CASES["sigmoid-E256k8g8"].replace(T=T)
     rng = np.random.default_rng(T)
     _check(moe, cfg, rng.standard_normal((T, 256)).astype(np.float32),
            (rng.standard_normal(256) * 0.1).astype(np.float32))
+
+
+@pytest.mark.parametrize("T", [1025, 4098])
+@pytest.mark.parametrize("name", ["softmax-E7k3g1", "softmax-E64k2g1", "softmax-E128k8g1",
+                                  "sigmoid-E65k8g1", "sigmoid-E256k8g8", "softmax-E24k6g4",
+                                  "sigmoid-E60k5g6", "sigmoid-E320k8g5", "softmax-E512k6g16",
+                                  "softmax-E33k11g11", "sigmoid-E200k32g1", "softmax-E16k4g16"])
+def test_larger_batches(moe, name, T):
+    """Several tokens a wave, masked experts and whole masked rows among them."""
+    cfg = CASES[name].replace(T=T)
+    rng = np.random.default_rng(T + cfg.E)
+    lg = rng.standard_normal((T, cfg.E)).astype(np.float32)
+    lg[rng.random((T, cfg.E)) < 0.2] = -np.inf
+    lg[::7] = np.finfo(np.float32).min
+    bias = (rng.standard_normal(cfg.E) * 0.1).astype(np.float32)
+    _check(moe, cfg, lg, bias, 2.5)
 
 
 def test_offset_views(moe):
