@@ -166,8 +166,11 @@ def _nbytes(t) -> int:
 
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # (a Stream object is 2.5 us of a small call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            return torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -282,72 +285,93 @@ def moe_layer_forward_w8a8(cfg, logits, x, w13_q, w13_scale, w2_q, w2_scale, sha
         "moe_layer_forward_w8a8")
 
 
-def _want(name, t, dtype, numel):
-    """A tensor of the type and at least the size that a call takes, on the
-    current device (addresses and None pass)."""
-    if t is None or isinstance(t, int):
-        return
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.numel() < numel:
-        raise ValueError(f"{name} must hold {numel} elements, not {t.numel()}")
-    if t.device.type == "cuda" and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is "
-                         f"cuda:{torch.cuda.current_device()}")
+def _args(*specs):
+    """Addresses of (name, tensor, dtype, numel): each of that type, at least
+    that many elements, contiguous and on the current device (addresses and
+    None pass as they are)."""
+    addresses, placed, last = [], [], None
+    for name, t, dtype, numel in specs:
+        if t is None or type(t) is int:
+            addresses.append(t)
+            continue
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+        if t.numel() < numel:
+            raise ValueError(f"{name} must hold {numel} elements, not {t.numel()}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.get_device() != last:   # (one check for a run of one device's)
+            last = t.get_device()
+            placed.append((name, t.device))
+        addresses.append(t.data_ptr())
+    for name, device in placed:
+        if device.type != "cuda":
+            raise ValueError(f"{name} must be on the GPU, not on {device}")
+        if device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+    return addresses
+
+
+def _workspace(t):
+    """Address and bytes of a workspace of any type."""
+    return (*_args(("workspace", t, t.dtype, 0)), _nbytes(t))
 
 
 def moe_route_biased(cfg, logits, bias, routed_scale, topk_ids, topk_w, stream=None):
     """Top-k routing on scores + bias (bias fp32 [E] or None), the weights
     from the scores, times routed_scale; empty slots get id -1, weight 0."""
     c = _cfg(cfg)
-    _want("logits", logits, torch.float32, c.T * c.E)
-    _want("bias", bias, torch.float32, c.E)
-    _want("topk_ids", topk_ids, torch.int32, c.T * c.k)
-    _want("topk_w", topk_w, torch.float32, c.T * c.k)
-    _check(lib.moe_route_biased(ctypes.byref(c), _ptr(logits), _ptr(bias), routed_scale,
-                                _ptr(topk_ids), _ptr(topk_w), _stream(stream)),
-           "moe_route_biased")
+    logits, bias, topk_ids, topk_w = _args(
+        ("logits", logits, torch.float32, c.T * c.E), ("bias", bias, torch.float32, c.E),
+        ("topk_ids", topk_ids, torch.int32, c.T * c.k),
+        ("topk_w", topk_w, torch.float32, c.T * c.k))
+    _check(lib.moe_route_biased(ctypes.byref(c), logits, bias, routed_scale, topk_ids, topk_w,
+                                _stream(stream)), "moe_route_biased")
 
 
 def _mx_rows(wide, q, scale):
-    """(dtype, rows, cols) of a conversion between wide [.., cols] and MXFP4."""
+    """dtype, rows and cols of a conversion between wide [.., cols] and MXFP4,
+    and the addresses of the three."""
     if wide.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"MXFP4 rows convert from and to float32 and bfloat16, not {wide.dtype}")
-    cols = wide.shape[-1]
-    _want("q", q, torch.uint8, wide.numel() // 2)
-    _want("scale", scale, torch.uint8, wide.numel() // 32)
-    _want("rows", wide, wide.dtype, 0)
-    return (MOE_DT_F32 if wide.dtype == torch.float32 else MOE_DT_BF16,
-            wide.numel() // cols if cols else 0, cols)
+    cols, n = wide.shape[-1], wide.numel()
+    dtype = MOE_DT_F32 if wide.dtype == torch.float32 else MOE_DT_BF16
+    return (dtype, n // cols if cols else 0, cols), _args(
+        ("rows", wide, wide.dtype, 0), ("q", q, torch.uint8, n // 2),
+        ("scale", scale, torch.uint8, n // 32))
 
 
 def moe_quantize_mxfp4(src, q, scale, stream=None):
     """src [.., cols] bf16 or fp32 -> q uint8 [.., cols/2] (two E2M1 codes a
     byte), scale uint8 [.., cols/32] (E8M0)."""
-    _check(lib.moe_quantize_mxfp4(*_mx_rows(src, q, scale), _ptr(src), _ptr(q), _ptr(scale),
-                                  _stream(stream)), "moe_quantize_mxfp4")
+    shape, (src, q, scale) = _mx_rows(src, q, scale)
+    _check(lib.moe_quantize_mxfp4(*shape, src, q, scale, _stream(stream)), "moe_quantize_mxfp4")
 
 
 def moe_dequantize_mxfp4(q, scale, dst, stream=None):
-    """q, scale as moe_quantize_mxfp4 writes them -> dst [.., cols] bf16 or fp32."""
-    _check(lib.moe_dequantize_mxfp4(*_mx_rows(dst, q, scale), _ptr(q), _ptr(scale), _ptr(dst),
-                                    _stream(stream)), "moe_dequantize_mxfp4")
+    """The values of MXFP4 rows, to dst [.., cols] bf16 or fp32."""
+    shape, (dst, q, scale) = _mx_rows(dst, q, scale)
+    _check(lib.moe_dequantize_mxfp4(*shape, q, scale, dst, _stream(stream)),
+           "moe_dequantize_mxfp4")
 
 
-def _want_mx_weights(c, I, n, w13_q, w13_scale, w2_q, w2_scale, name=""):
-    """n experts of intermediate size I in MXFP4."""
-    for what, t, numel in (("w13_q", w13_q, n * I * c.H), ("w13_scale", w13_scale, n * I * c.H // 16),
-                           ("w2_q", w2_q, n * I * c.H // 2),
-                           ("w2_scale", w2_scale, n * I * c.H // 32)):
-        _want(name + what, t, torch.uint8, numel)
+def _mx_weights(c, I, n, w13_q, w13_scale, w2_q, w2_scale, name=""):
+    """The specs of n experts of intermediate size I in MXFP4."""
+    return ((name + "w13_q", w13_q, torch.uint8, n * I * c.H),
+            (name + "w13_scale", w13_scale, torch.uint8, n * I * c.H // 16),
+            (name + "w2_q", w2_q, torch.uint8, n * I * c.H // 2),
+            (name + "w2_scale", w2_scale, torch.uint8, n * I * c.H // 32))
 
 
-def _want_ffn(c, seg_offsets, seg_expert, row_scale, y_perm):
+def _mx_ffn(c, x, seg_offsets, seg_expert, weights, row_scale, y_perm):
+    """The addresses of a grouped FFN's tensors (x: the specs of its rows)."""
     S, R = moe_num_segments(c), moe_num_rows(c)
-    _want("seg_offsets", seg_offsets, torch.int32, S + 1)
-    _want("seg_expert", seg_expert, torch.int32, S)
-    _want("row_scale", row_scale, torch.float32, R)
-    _want("y_perm", y_perm, torch.bfloat16, R * c.H)
+    return _args(*x(R), ("seg_offsets", seg_offsets, torch.int32, S + 1),
+                 ("seg_expert", seg_expert, torch.int32, S),
+                 *_mx_weights(c, c.I, c.E, *weights),
+                 ("row_scale", row_scale, torch.float32, R),
+                 ("y_perm", y_perm, torch.bfloat16, R * c.H))
 
 
 def moe_grouped_ffn_mxfp4w(cfg, x_perm, seg_offsets, seg_expert, w13_q, w13_scale, w2_q, w2_scale,
@@ -355,14 +379,10 @@ def moe_grouped_ffn_mxfp4w(cfg, x_perm, seg_offsets, seg_expert, w13_q, w13_scal
     """moe_grouped_ffn on MXFP4 weights: w13_q uint8 [E, 2I, H/2] + w13_scale
     uint8 [E, 2I, H/32], w2_q [E, H, I/2] + w2_scale [E, H, I/32]."""
     c = _cfg(cfg)
-    _want("x_perm", x_perm, torch.bfloat16, moe_num_rows(c) * c.H)
-    _want_ffn(c, seg_offsets, seg_expert, row_scale, y_perm)
-    _want_mx_weights(c, c.I, c.E, w13_q, w13_scale, w2_q, w2_scale)
-    _check(lib.moe_grouped_ffn_mxfp4w(ctypes.byref(c), _ptr(x_perm), _ptr(seg_offsets),
-                                      _ptr(seg_expert), _ptr(w13_q), _ptr(w13_scale), _ptr(w2_q),
-                                      _ptr(w2_scale), _ptr(row_scale), _ptr(y_perm),
-                                      _ptr(workspace), _nbytes(workspace), _stream(stream)),
-           "moe_grouped_ffn_mxfp4w")
+    a = _mx_ffn(c, lambda R: (("x_perm", x_perm, torch.bfloat16, R * c.H),), seg_offsets,
+                seg_expert, (w13_q, w13_scale, w2_q, w2_scale), row_scale, y_perm)
+    _check(lib.moe_grouped_ffn_mxfp4w(ctypes.byref(c), *a, *_workspace(workspace),
+                                      _stream(stream)), "moe_grouped_ffn_mxfp4w")
 
 
 def moe_grouped_ffn_w4a4(cfg, x_perm_q, x_perm_scale, seg_offsets, seg_expert, w13_q, w13_scale,
@@ -370,35 +390,26 @@ def moe_grouped_ffn_w4a4(cfg, x_perm_q, x_perm_scale, seg_offsets, seg_expert, w
     """moe_grouped_ffn_mxfp4w on MXFP4 rows: x_perm_q uint8 [R, H/2] +
     x_perm_scale uint8 [R, H/32]."""
     c = _cfg(cfg)
-    R = moe_num_rows(c)
-    _want("x_perm_q", x_perm_q, torch.uint8, R * c.H // 2)
-    _want("x_perm_scale", x_perm_scale, torch.uint8, R * c.H // 32)
-    _want_ffn(c, seg_offsets, seg_expert, row_scale, y_perm)
-    _want_mx_weights(c, c.I, c.E, w13_q, w13_scale, w2_q, w2_scale)
-    _check(lib.moe_grouped_ffn_w4a4(ctypes.byref(c), _ptr(x_perm_q), _ptr(x_perm_scale),
-                                    _ptr(seg_offsets), _ptr(seg_expert), _ptr(w13_q),
-                                    _ptr(w13_scale), _ptr(w2_q), _ptr(w2_scale), _ptr(row_scale),
-                                    _ptr(y_perm), _ptr(workspace), _nbytes(workspace),
-                                    _stream(stream)),
-           "moe_grouped_ffn_w4a4")
+    a = _mx_ffn(c, lambda R: (("x_perm_q", x_perm_q, torch.uint8, R * c.H // 2),
+                              ("x_perm_scale", x_perm_scale, torch.uint8, R * c.H // 32)),
+                seg_offsets, seg_expert, (w13_q, w13_scale, w2_q, w2_scale), row_scale, y_perm)
+    _check(lib.moe_grouped_ffn_w4a4(ctypes.byref(c), *a, *_workspace(workspace),
+                                    _stream(stream)), "moe_grouped_ffn_w4a4")
 
 
 def _mx_layer(fn, where, cfg, logits, route_bias, routed_scale, x, w, sw, out, topk_ids, topk_w,
               counts, balancedness, workspace, stream):
     c = _cfg(cfg)
-    _want("logits", logits, torch.float32, c.T * c.E)
-    _want("route_bias", route_bias, torch.float32, c.E)
-    _want("x", x, torch.bfloat16, c.T * c.H)
-    _want("out", out, torch.bfloat16, c.T * c.H)
-    _want("topk_ids", topk_ids, torch.int32, c.T * c.k)
-    _want("topk_w", topk_w, torch.float32, c.T * c.k)
-    _want("counts", counts, torch.int32, c.E)
-    _want("balancedness", balancedness, torch.float32, 1)
-    _want_mx_weights(c, c.I, c.E, *w)
-    _want_mx_weights(c, c.shared_I, 1, *sw, name="shared_")
-    _check(fn(ctypes.byref(c), _ptr(logits), _ptr(route_bias), routed_scale, _ptr(x),
-              *map(_ptr, w), *map(_ptr, sw), _ptr(out), _ptr(topk_ids), _ptr(topk_w),
-              _ptr(counts), _ptr(balancedness), _ptr(workspace), _nbytes(workspace),
+    logits, route_bias, *rest = _args(
+        ("logits", logits, torch.float32, c.T * c.E),
+        ("route_bias", route_bias, torch.float32, c.E),
+        ("x", x, torch.bfloat16, c.T * c.H), *_mx_weights(c, c.I, c.E, *w),
+        *_mx_weights(c, c.shared_I, 1, *sw, name="shared_"),
+        ("out", out, torch.bfloat16, c.T * c.H),
+        ("topk_ids", topk_ids, torch.int32, c.T * c.k),
+        ("topk_w", topk_w, torch.float32, c.T * c.k), ("counts", counts, torch.int32, c.E),
+        ("balancedness", balancedness, torch.float32, 1))
+    _check(fn(ctypes.byref(c), logits, route_bias, routed_scale, *rest, *_workspace(workspace),
               _stream(stream)), where)
 
 
