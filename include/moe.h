@@ -411,7 +411,7 @@ moe_status moe_route_biased(const moe_config* cfg, const float* logits, const fl
  *   src [rows, cols] 16-byte aligned; q [rows, cols/2] out, 16-byte aligned;
  *   scale [rows, cols/32] out, 4-byte aligned.
  * MOE_ERR_INVALID_ARG for bad sizes, types or pointers, MOE_ERR_UNSUPPORTED
- * beyond 2^40 elements; rows == 0 is MOE_OK; asynchronous on `stream`. */
+ * beyond 2^34 elements; rows == 0 is MOE_OK; asynchronous on `stream`. */
 moe_status moe_quantize_mxfp4(int32_t dtype, int64_t rows, int32_t cols, const void* src,
                               uint8_t* q, uint8_t* scale, void* stream);
 

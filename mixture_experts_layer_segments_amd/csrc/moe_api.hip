@@ -628,8 +628,8 @@ int check_mx_rows(int32_t dtype, int64_t rows, int32_t cols, const void* wide, c
                   const void* scale) {
   if (dtype != MOE_DT_BF16 && dtype != MOE_DT_F32) return MOE_ERR_INVALID_ARG;
   if (rows < 0 || cols <= 0 || cols % 32) return MOE_ERR_INVALID_ARG;
-  // (one thread per 8 elements, 256 a workgroup, within the grid's 32 bits)
-  if (rows > ((int64_t)1 << 40) / cols) return MOE_ERR_UNSUPPORTED;
+  // (one thread per 8 elements, and a launch holds less than 2^32 threads)
+  if (rows > ((int64_t)1 << 34) / cols) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!wide || !q || !scale || !aligned(wide, 16) || !aligned(q, 16) || !aligned(scale, 4))
     return MOE_ERR_INVALID_ARG;

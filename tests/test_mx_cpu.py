@@ -63,6 +63,7 @@ def test_row_conversion_refusals(call, wide_at):
     assert go(1, 4, 32, q=FAKE + 4) == -1
     assert go(1, 4, 32, s=FAKE + 1) == -1
     assert go(1, 1 << 40, 64) == -2
+    assert go(1, (1 << 29) + 1, 32) == -2
     assert go(0, 0, 32, None, None, None) == 0
 
 
