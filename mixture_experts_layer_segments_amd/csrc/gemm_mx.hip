@@ -47,16 +47,19 @@ struct MxArgs {
 };
 
 // silu(z) = z / (1 + e^-z) with the hardware's base-2 exponential and
-// reciprocal: e^-z = 2^(h + l), h the rounded product z * -log2 e and l what
-// its rounding and the constant's left out, so that large |z| lose nothing
-// (about 2^-22 in all; h is rounded to bf16 next).  (expf and a division were
-// a quarter of a 256-row FP4 tile's epilogue.)
+// reciprocal: e^-z = 2^h (1 + l ln 2), h the rounded product z * -log2 e and l
+// what its rounding and the constant's left out, so that large |z| lose
+// nothing (about 2^-22 in all; h is rounded to bf16 next).  The exponent's z is
+// held to +-200, where e^-z is 0 or infinity already, so that no infinity
+// meets another.  The reciprocal has no subnormals: below z = -87 the result
+// is 0 where the formula's is within 1e-36.
 __device__ __forceinline__ float silu_fast(float z) {
   constexpr float c = -1.44269504f, cl = -1.92596299e-8f;
-  const float h = z * c;
-  const float l = fmaf(z, cl, fmaf(z, c, -h));
-  const float e = __builtin_amdgcn_exp2f(h);
-  return z * __builtin_amdgcn_rcpf(1.0f + fmaf(e, l * 0.693147182f, e));
+  const float x = __builtin_amdgcn_fmed3f(z, -200.0f, 200.0f);
+  const float h = x * c;
+  const float l = fmaf(x, cl, fmaf(x, c, -h));
+  const float e = __builtin_amdgcn_exp2f(h) * fmaf(l, 0.693147182f, 1.0f);
+  return z * __builtin_amdgcn_rcpf(1.0f + e);
 }
 
 // ---------------------------------------------------------------- streaming tiles
@@ -954,6 +957,11 @@ bool launch_ring(const MxArgs& g, hipStream_t s) {
   k<<<persistent_grid(k, dyn, 1, 512), 512, dyn, s>>>(g);
   return true;
 }
+
+// (the smallest rings fit beside the longest table: routed and shared segments)
+static_assert(mx_ring_lds<true, 2, false>() * 16 + (kMaxSegments + 2) * 4 + 64 <= kMaxLdsBytes &&
+                  mx_ring_lds<false, 2, false>() * 16 + (kMaxSegments + 2) * 4 + 64 <= kMaxLdsBytes,
+              "every launch has a ring");
 
 template <int MODE, bool AF4>
 void launch_gemm(const MxArgs& g, bool few_rows, int longest, hipStream_t s) {

@@ -96,6 +96,22 @@ def test_rows_every_scale_reads_back(moe):
         np.testing.assert_array_equal(back.float().cpu().numpy(), ref32)
 
 
+def test_rows_beyond_the_caches(moe):
+    """A result of more than 128 MB: the bf16 values are the fp32 ones."""
+    rows, cols = 16411, 4128
+    g = torch.Generator(device=gu.dev()).manual_seed(4)
+    q = torch.randint(0, 256, (rows, cols // 2), dtype=torch.uint8, device=gu.dev(), generator=g)
+    s = torch.randint(100, 160, (rows, cols // 32), dtype=torch.uint8, device=gu.dev(), generator=g)
+    wide = torch.empty((rows, cols), device=gu.dev())
+    half = torch.full((rows + 1, cols), 7.0, dtype=torch.bfloat16, device=gu.dev())
+    moe.moe_dequantize_mxfp4(q, s, wide)
+    moe.moe_dequantize_mxfp4(q, s, half[:rows])
+    assert torch.equal(half[:rows].float(), wide)
+    assert (half[rows] == 7).all()
+    ref = omx.dequantize_rows(omx.unpack(q[-3:].cpu().numpy()), s[-3:].cpu().numpy())
+    np.testing.assert_array_equal(wide[-3:].cpu().numpy(), ref)
+
+
 # ------------------------------------------------------------------ experts
 def _segments(lens):
     return torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32,
@@ -184,6 +200,77 @@ def test_nan_and_inf_stay_in_their_rows(moe, a4):
     np.testing.assert_array_equal(got[:5], clean[:5])
     np.testing.assert_array_equal(got[45:], clean[45:])
     assert np.isnan(got[5:45]).any(1).all()
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+@pytest.mark.parametrize("rows", [4, 60, 200, 300])
+def test_large_gates(moe, rows, a4):
+    """Gates from about -600 to 600: e^-z overflows and underflows."""
+    rng = np.random.default_rng(rows)
+    cfg = mi.MoEShape("g", T=2 * rows, H=256, E=2, k=1, I=256)
+    ex = mu.Experts(rng, 2, 256, 256, std=3.0)
+    x = mu.bf16_rows(rng, 2 * rows, 256)
+    x[0], x[rows, 1:] = 0, 0
+    y = _run_ffn(moe, cfg, ex, x, [rows, rows], [1, 0], None, a4)
+    for s, e in enumerate((1, 0)):
+        sl = slice(s * rows, (s + 1) * rows)
+        gate = x[sl] @ ex.w13[e][:256].T
+        assert gate.min() < -150 and gate.max() > 150
+        mu.check_close(y[sl], *mu.expert_tol(x[sl], ex.w13[e], ex.w2[e], a4), f"expert {e}")
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+def test_infinite_gates(moe, a4):
+    """silu(inf) = inf; a gate of -inf has no value (-inf times 0)."""
+    rng = np.random.default_rng(2)
+    cfg = mi.MoEShape("g", T=40, H=128, E=1, k=1, I=128)
+    ex = mu.Experts(rng, 1, 128, 128)
+    # hidden unit 0: gate = x_0 * 2^100, up = x_1
+    ex.q13[0, [0, 128]], ex.s13[0, [0, 128]] = 0, 127
+    ex.q13[0, 0, 0], ex.s13[0, 0, 0] = 2, 227        # code 2 = 1.0 at element 0
+    ex.q13[0, 128, 0] = 2 << 4                       # 1.0 at element 1
+    x = mu.bf16_rows(rng, 40, 128)
+    x[:, 0] = 0.0
+    clean = _run_ffn(moe, cfg, ex, x, [40], [0], None, a4)
+    assert np.isfinite(clean).all()
+    x[3, :2], x[37, :2] = 2.0 ** 100, 2.0 ** 100
+    got = _run_ffn(moe, cfg, ex, x, [40], [0], None, a4)
+    other = np.setdiff1d(np.arange(40), [3, 37])
+    np.testing.assert_array_equal(got[other], clean[other])
+    assert not np.isfinite(got[[3, 37]]).any(1).all()
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+@pytest.mark.parametrize("n,hot,ways", [(1000, 0, 1), (1024, 0, 1), (600, 600, 2), (1024, 1024, 4)])
+def test_many_segments(moe, n, hot, ways, a4):
+    """More segments than the larger rings leave room for: every length class
+    and empty segments among them."""
+    rng = np.random.default_rng(n + ways)
+    H = I = 128
+    S = n + hot * (ways - 1)
+    L = rng.integers(0, 38, S)
+    L[[1, S // 2, S - 1]] = 300, 257, 130
+    cfg = mi.MoEShape("s", T=int(L.sum()) + 3, H=H, E=n, k=1, I=I, n_hot_split=hot,
+                      split_ways=ways)
+    assert moe.moe_num_segments(cfg) == S and L.sum() > 16 * S
+    few = mu.Experts(rng, 8, H, I)
+
+    class All:
+        def device(self):
+            out = []
+            for t in few.device():
+                a = torch.zeros((n,) + t.shape[1:], dtype=torch.uint8, device=t.device)
+                a[-8:] = t
+                out.append(a)
+            return tuple(out)
+    expert = rng.integers(0, 8, S)
+    x = mu.bf16_rows(rng, int(L.sum()), H)
+    y = _run_ffn(moe, cfg, All(), x, L, n - 8 + expert, None, a4)
+    row_expert = np.repeat(expert, L)
+    for e in range(8):
+        rows = np.nonzero(row_expert == e)[0]
+        mu.check_close(y[rows], *mu.expert_tol(x[rows], few.w13[e], few.w2[e], a4), f"expert {e}")
+    assert (y[L.sum():] == 7).all()
 
 
 @pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
