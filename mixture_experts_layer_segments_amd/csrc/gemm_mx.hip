@@ -44,6 +44,7 @@ struct MxArgs {
   int32_t n_probs;
   int32_t n_seg_total;
   int32_t tile_bm, tile_ncols, min_len, max_len;   // as GemmArgs
+  int32_t* queue;   // ring tiles: [kMxClasses][8], the next tile of each XCD
 };
 
 // silu(z) = z / (1 + e^-z) with the hardware's base-2 exponential and
@@ -60,6 +61,13 @@ __device__ __forceinline__ float silu_fast(float z) {
   const float l = fmaf(x, cl, fmaf(x, c, -h));
   const float e = __builtin_amdgcn_exp2f(h) * fmaf(l, 0.693147182f, 1.0f);
   return z * __builtin_amdgcn_rcpf(1.0f + e);
+}
+
+// Two bf16 in one conversion.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 // ---------------------------------------------------------------- streaming tiles
@@ -414,48 +422,41 @@ struct MxRing {
   static_assert(STAGES == 2 || STAGES == 3, "stage waits");
 };
 
-// Where a tile sits and this lane's copy sources (byte offsets at k = 0; the
-// weight copies of a wave lie at uniform distances).
-template <typename R>
-struct MxTile {
+// Where a tile sits: values of the whole workgroup.
+struct MxPlace {
   // (the problem by its number: a pointer into the kernel's arguments, carried
   // around the tile loop, had them copied to scratch memory)
-  int pi, K, up_off, r0, len, m0, n0;
-  bool stream;
-  __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
-  uint32_t va[R::A_IT], vb, vsa, vsb;
+  int pi, e, r0, len, m0, n0;
 };
 
-template <int MODE, bool AF4, typename R, int BM>
-__device__ __forceinline__ void mx_ring_setup(const MxArgs& args, const int* tiles_l, int tile,
-                                              MxTile<R>& t) {
-  const int lane = threadIdx.x & 63;
-  const int wvs = uniform(threadIdx.x >> 6);
+// Reads a value of the whole workgroup that no kernel of this launch writes:
+// by the scalar unit, beside the vector memory operations in flight.
+__device__ __forceinline__ int scalar_load(const int32_t* p) {
+  return *(const __attribute__((address_space(4))) int32_t*)(uintptr_t)p;
+}
+
+template <int MODE, int BM>
+__device__ __forceinline__ MxPlace mx_ring_place(const MxArgs& args, const int* tiles_l, int tile) {
+  MxPlace t;
   int lo = 0, hi = args.n_seg_total - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (tiles_l[mid] <= tile) lo = mid; else hi = mid - 1;
+    if (uniform(tiles_l[mid]) <= tile) lo = mid; else hi = mid - 1;
   }
-  lo = uniform(lo);
-  const int pi = lo < args.p[0].n_seg ? 0 : 1;
-  const MxProblem& P = args.p[pi];
-  t.pi = pi;
-  t.K = P.K;
-  t.up_off = P.up_off;
+  t.pi = lo < args.p[0].n_seg ? 0 : 1;
+  const MxProblem& P = args.p[t.pi];
   t.r0 = 0;
   t.len = P.rows;
-  int e = 0;
+  t.e = 0;
   if (P.seg_offsets) {
-    const int s = lo - (pi ? args.p[0].n_seg : 0);
-    t.r0 = uniform(P.seg_offsets[s]);
-    t.len = uniform(P.seg_offsets[s + 1]) - t.r0;
-    e = uniform(P.seg_expert[s]);
+    const int s = lo - (t.pi ? args.p[0].n_seg : 0);
+    t.r0 = scalar_load(P.seg_offsets + s);
+    t.len = scalar_load(P.seg_offsets + s + 1) - t.r0;
+    t.e = scalar_load(P.seg_expert + s);
   }
   const int mt = (t.len + BM - 1) / BM;
-  t.stream = mt == 1;
-  constexpr int ncols = MODE == 0 ? R::BN / 2 : R::BN;
-  const int K = P.K, N = P.N;
-  const int nt = (N + ncols - 1) / ncols;
+  constexpr int ncols = MODE == 0 ? 128 : 256;
+  const int nt = (P.N + ncols - 1) / ncols;
   const int local = tile - uniform(tiles_l[lo]);
   const int grp = local / (kGroupM * nt);
   const int first_m = grp * kGroupM;
@@ -463,14 +464,57 @@ __device__ __forceinline__ void mx_ring_setup(const MxArgs& args, const int* til
   const int lg = local - grp * kGroupM * nt;
   t.m0 = (first_m + lg % gm) * BM;
   t.n0 = (lg / gm) * ncols;
+  return t;
+}
+
+// The tiles of a class are divided among the XCDs as a static launch would do
+// it, rounds of gridDim.x neighbouring tiles in eight parts and what is left
+// over evenly, and a workgroup takes the next of its XCD's: the j-th, or -1.
+__device__ __forceinline__ int mx_queue_tile(int j, int total) {
+  const int G = gridDim.x, per = G / 8, x = blockIdx.x % 8;
+  const int full = total / G, rem = total - full * G;
+  if (j < full * per) return j / per * G + x * per + j % per;
+  const int at = rem * x / 8 + (j - full * per);
+  return at < rem * (x + 1) / 8 ? full * G + at : -1;
+}
+
+// A tile and this lane's copy sources (byte offsets at k = 0; the weight
+// copies of a wave lie at uniform distances).
+template <typename R>
+struct MxTile : MxPlace {
+  int K, up_off;
+  bool stream;
+  __amdgpu_buffer_rsrc_t ra, rb, rsa, rsb;
+  uint32_t va[R::A_IT], vb, vsa, vsb;
+  float rs[R::TM];          // GEMM 2: the scales of this lane's output rows
+};
+
+template <int MODE, bool AF4, typename R, int BM>
+__device__ __forceinline__ void mx_ring_setup(const MxArgs& args, const MxPlace& at,
+                                              MxTile<R>& t) {
+  const int lane = threadIdx.x & 63;
+  const int wvs = uniform(threadIdx.x >> 6);
+  static_cast<MxPlace&>(t) = at;
+  const MxProblem& P = args.p[t.pi];
+  t.K = P.K;
+  t.up_off = P.up_off;
+  t.stream = t.len <= BM;
+  const int K = P.K;
   const uint32_t arow_b = AF4 ? K / 2 : K * 2, brow_b = K / 2, srow_b = K / 32;
-  const int64_t e_row = (int64_t)e * P.b_rows;
+  const int64_t e_row = (int64_t)t.e * P.b_rows;
   // (weight rows past the expert's last -- the last column tile of a GEMM 2
   // whose N is an odd multiple of 128 -- lie past the buffers: zeros)
   t.ra = buffer_rsrc(P.A, (uint32_t)((size_t)P.a_ld_rows * arow_b));
   t.rb = buffer_rsrc(P.B + e_row * brow_b, (uint32_t)((size_t)P.b_rows * brow_b));
   if constexpr (AF4) t.rsa = buffer_rsrc(P.a_e8, (uint32_t)((size_t)P.a_ld_rows * srow_b));
   t.rsb = buffer_rsrc(P.b_e8 + e_row * srow_b, (uint32_t)((size_t)P.b_rows * srow_b));
+  if constexpr (MODE == 1) {
+#pragma unroll
+    for (int mi = 0; mi < R::TM; ++mi) {
+      const int row = t.m0 + (mi * R::WAVES_M + wvs / R::WAVES_N) * 16 + (lane & 15);
+      t.rs[mi] = P.scale ? P.scale[t.r0 + min(row, t.len - 1)] : 1.0f;
+    }
+  }
   if (wvs >= R::NI) return;
   auto a_src = [&](int row) -> uint32_t {
     const int ar = t.r0 + min(t.m0 + row, t.len - 1);
@@ -539,15 +583,27 @@ __device__ __forceinline__ void mx_ring_prologue(const MxTile<R>& t, u32x4* ring
 }
 
 // Waits until stage kt of KT has landed: at most the copies of the stage
-// after it (three stages) may be outstanding.
-template <typename R>
-__device__ __forceinline__ void mx_ring_wait(int kt, int KT) {
-  if constexpr (R::STAGES == 2) {
+// after it (three stages) may be outstanding and, where `stores` stores of the
+// tile before were issued behind this tile's first stages, those too.
+// (Vector memory operations of a wave complete in the order of their issue.)
+template <typename R, int STORES>
+__device__ __forceinline__ void mx_ring_wait(int kt, int KT, bool stores) {
+  constexpr int LPI = R::LPI;
+  if (stores && kt < R::STAGES - 1) {
+    if constexpr (R::STAGES == 2) {
+      wait_vmcnt<STORES>();
+    } else if (kt == 0) {
+      if (KT > 1) wait_vmcnt<STORES + LPI>(); else wait_vmcnt<STORES>();
+    } else {
+      if (KT > 2) wait_vmcnt<STORES + LPI + (2 % R::SG == 0 ? R::S_IT : 0)>();
+      else wait_vmcnt<STORES>();
+    }
+  } else if constexpr (R::STAGES == 2) {
     wait_vmcnt<0>();
   } else {
     if (kt + 1 >= KT) wait_vmcnt<0>();
-    else if ((kt + 1) % R::SG == 0) wait_vmcnt<R::LPI + R::S_IT>();
-    else wait_vmcnt<R::LPI>();
+    else if ((kt + 1) % R::SG == 0) wait_vmcnt<LPI + R::S_IT>();
+    else wait_vmcnt<LPI>();
   }
 }
 
@@ -670,15 +726,28 @@ __device__ __forceinline__ void mx_ring_mma(const u32x4* ring, int kt, int wm, i
   }
 }
 
+// Column parts of the output's staging, and the stores that a wave issues.
+template <int MODE, typename R, int BM>
+constexpr int mx_ring_passes() {
+  return BM * (MODE == 0 ? R::BN / 2 : R::BN) / 8 > R::STAGE_CH ? 2 : 1;
+}
+template <int MODE, bool AF4, typename R, int BM>
+constexpr int mx_ring_stores() {
+  // FP4 h: codes and scales of 32 rows at a time; else 1 KiB a store
+  if (MODE == 0 && AF4) return BM / 32 * 2;
+  return R::WM * (MODE == 0 ? R::WN / 2 : R::WN) * 2 / 1024;
+}
+
 // The K loop of one tile over the wave's NM live row fragments (0: copies and
 // barriers only).  (One loop for each NM, chosen outside it: variants inside
 // one loop cost a second set of accumulators where they meet.)
 template <int MODE, bool AF4, typename R, int BM, int NM>
 __device__ __forceinline__ void mx_ring_kloop(const MxTile<R>& t, u32x4* ring, int wm, int wn,
-                                              int wvs, int lane, f32x4 (&acc)[R::TM][R::TN]) {
+                                              int wvs, int lane, bool stores,
+                                              f32x4 (&acc)[R::TM][R::TN]) {
   const int K = t.K, KT = (K + R::BK - 1) / R::BK;
   auto enter = [&](int kt) {
-    if (wvs < R::NI) mx_ring_wait<R>(kt, KT);
+    if (wvs < R::NI) mx_ring_wait<R, mx_ring_stores<MODE, AF4, R, BM>()>(kt, KT, stores);
     raw_barrier();
     if (kt + R::STAGES - 1 < KT && wvs < R::NI)
       mx_ring_stage<MODE, AF4, R, BM>(t, ring, kt + R::STAGES - 1, wvs);
@@ -696,13 +765,14 @@ __device__ __forceinline__ void mx_ring_kloop(const MxTile<R>& t, u32x4* ring, i
 
 template <int MODE, bool AF4, typename R, int BM, int NM = R::TM>
 __device__ __forceinline__ void mx_ring_kloop_live(const MxTile<R>& t, u32x4* ring, int wm, int wn,
-                                                   int wvs, int lane, int live,
+                                                   int wvs, int lane, int live, bool stores,
                                                    f32x4 (&acc)[R::TM][R::TN]) {
   if constexpr (NM > 0) {
     if (live < NM)
-      return mx_ring_kloop_live<MODE, AF4, R, BM, NM - 1>(t, ring, wm, wn, wvs, lane, live, acc);
+      return mx_ring_kloop_live<MODE, AF4, R, BM, NM - 1>(t, ring, wm, wn, wvs, lane, live, stores,
+                                                          acc);
   }
-  mx_ring_kloop<MODE, AF4, R, BM, NM>(t, ring, wm, wn, wvs, lane, acc);
+  mx_ring_kloop<MODE, AF4, R, BM, NM>(t, ring, wm, wn, wvs, lane, stores, acc);
 }
 
 // The tile's output through the free ring slot: every wave stages its rows in
@@ -717,7 +787,7 @@ __device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R
                                               const u32x2* out, u32x4* slot) {
   constexpr int TM = R::TM, WM = R::WM, NPM = MODE == 0 ? R::TN / 2 : R::TN;
   constexpr int COUT = MODE == 0 ? R::WN / 2 : R::WN;
-  constexpr int PASSES = BM * (MODE == 0 ? R::BN / 2 : R::BN) / 8 > R::STAGE_CH ? 2 : 1;
+  constexpr int PASSES = mx_ring_passes<MODE, R, BM>();
   constexpr int NP = NPM / PASSES, CPR = COUT / PASSES / 8, RPI = 64 / CPR;
   static_assert(CPR <= 16 && 64 % CPR == 0 && WM % RPI == 0, "output transpose shape");
   static_assert(8 * WM * CPR <= R::STAGE_CH, "the staged output fits a slot");
@@ -745,6 +815,8 @@ __device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R
       raw_barrier();   // every wave's rows are staged
       const __amdgpu_buffer_rsrc_t rq =
           buffer_rsrc(P.Cq + (size_t)t.r0 * (N / 2), (uint32_t)((size_t)t.len * (N / 2)));
+      const __amdgpu_buffer_rsrc_t re =
+          buffer_rsrc(P.c_e8 + (size_t)t.r0 * (N / 32), (uint32_t)((size_t)t.len * (N / 32)));
       int tid = threadIdx.x;
       asm volatile("" : "+v"(tid));
       const int cc = tid & 15;                          // this lane's 8 of the 128 columns
@@ -774,8 +846,9 @@ __device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R
                                  ? ((uint32_t)grow * (uint32_t)N + (uint32_t)(t.n0 + cc * 8)) / 2u
                                  : 0xFFFFFFF0u;
         __builtin_amdgcn_raw_buffer_store_b32(codes, rq, off, 0, 0);
-        if ((cc & 3) == 0 && grow < t.len)
-          P.c_e8[(size_t)(t.r0 + grow) * (N / 32) + (t.n0 + cc * 8) / 32] = (uint8_t)b;
+        // (no branch: the waits count every wave's stores)
+        __builtin_amdgcn_raw_buffer_store_b8((uint8_t)b, re, (cc & 3) == 0 ? off / 16u : 0xFFFFFFF0u,
+                                             0, 0);
       }
     } else {
       wave_lds_fence();
@@ -808,12 +881,20 @@ constexpr int mx_ring_lds() {
 }
 
 // Every tile of one class: the segments of [min_len, max_len) rows on tiles of
-// BM rows.  This workgroup takes tiles first, first + G, ...
+// BM rows, from the class's queue.  The last wave, which issues no copies,
+// fetches a tile's number and looks it up while the tile before is computed,
+// and leaves the place in `mail`.
 template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
 __device__ __forceinline__ void mx_ring_class(const MxArgs& args, u32x4* ring, int* tiles_l,
-                                              int min_len, int max_len, int first) {
+                                              int min_len, int max_len, int32_t* queue) {
   using R = MxRing<AF4, BM, STAGES, WAVES_M>;
   constexpr int TM = R::TM, TN = R::TN, NPM = MODE == 0 ? TN / 2 : TN;
+  constexpr int kFetch = 7;
+  const bool fetcher = threadIdx.x == kFetch * 64;
+  auto fetch = [&]() -> int {
+    return fetcher ? __hip_atomic_fetch_add(queue, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+  };
+  int ticket = fetch();
   __syncthreads();   // (the class before has left the LDS)
   // (the table's scan borrows the idle ring)
   build_tile_table<512>(args, tiles_l, reinterpret_cast<int*>(ring), BM,
@@ -822,14 +903,37 @@ __device__ __forceinline__ void mx_ring_class(const MxArgs& args, u32x4* ring, i
   const int lane = threadIdx.x & 63;
   const int wvs = uniform(threadIdx.x >> 6);
   const int wm = wvs / R::WAVES_N, wn = wvs % R::WAVES_N;
-  const int G = gridDim.x;
-  int tile = first;
-  if (tile >= total) return;
+  // (two slots in turn: a slow wave may still read one while the next is left)
+  int* mail = tiles_l + args.n_seg_total + 1;
+  auto post = [&](int slot) {
+    const int tile = mx_queue_tile(uniform(ticket), total);
+    MxPlace at{-1, 0, 0, 0, 0, 0};
+    if (tile >= 0) at = mx_ring_place<MODE, BM>(args, tiles_l, tile);
+    if (lane == 0) {
+      int* m = mail + slot * 6;
+      m[0] = at.pi;
+      m[1] = at.e;
+      m[2] = at.r0;
+      m[3] = at.len;
+      m[4] = at.m0;
+      m[5] = at.n0;
+    }
+  };
+  auto read_mail = [&](int slot) -> MxPlace {
+    const int* m = mail + slot * 6;
+    return {uniform(m[0]), uniform(m[1]), uniform(m[2]), uniform(m[3]), uniform(m[4]), uniform(m[5])};
+  };
+  if (wvs == kFetch) post(1);
+  __syncthreads();   // (and the table's scan has left the ring)
+  MxPlace next = read_mail(1);
+  if (next.pi < 0) return;
   MxTile<R> t;
-  mx_ring_setup<MODE, AF4, R, BM>(args, tiles_l, tile, t);
-  raw_barrier();   // (the table's scan has left the ring)
+  mx_ring_setup<MODE, AF4, R, BM>(args, next, t);
   if (wvs < R::NI) mx_ring_prologue<MODE, AF4, R, BM>(t, ring, wvs);
-  for (;;) {
+  ticket = fetch();
+  bool stores = false;
+  for (int slot = 0;; slot ^= 1) {
+    if (wvs == kFetch) post(slot);
     u32x2 outv[TM * NPM];
     {
       f32x4 acc[TM][TN];
@@ -841,73 +945,88 @@ __device__ __forceinline__ void mx_ring_class(const MxArgs& args, u32x4* ring, i
       // none takes part in the copies and barriers only)
       const int live =
           min(TM, ((t.len - t.m0 + 15) / 16 - wm + R::WAVES_M - 1) / R::WAVES_M);
-      mx_ring_kloop_live<MODE, AF4, R, BM>(t, ring, wm, wn, wvs, lane, live, acc);
+      mx_ring_kloop_live<MODE, AF4, R, BM>(t, ring, wm, wn, wvs, lane, live, stores, acc);
+      // (waited for here: the output is formed behind the next tile's copies,
+      // where the wait would be one for the copies)
+      if constexpr (MODE == 1) {
+#pragma unroll
+        for (int mi = 0; mi < TM; ++mi) asm volatile("" : "+v"(t.rs[mi]));
+      }
 #pragma unroll
       for (int mi = 0; mi < TM; ++mi) {
-        float rs = 1.0f;
-        const float* scale = args.p[t.pi].scale;
-        if (MODE == 1 && scale) {
-          const int row = t.m0 + (mi * R::WAVES_M + wm) * 16 + (lane & 15);
-          rs = scale[t.r0 + min(row, t.len - 1)];
-        }
 #pragma unroll
         for (int ni = 0; ni < NPM; ++ni) {
           if (MODE == 0) {
             const f32x4 g = acc[mi][ni], u = acc[mi][ni + TN / 2];
             outv[mi * NPM + ni] =
-                u32x2{pack_bf16x2(silu_fast(g[0]) * u[0], silu_fast(g[1]) * u[1]),
-                      pack_bf16x2(silu_fast(g[2]) * u[2], silu_fast(g[3]) * u[3])};
+                u32x2{pack2(silu_fast(g[0]) * u[0], silu_fast(g[1]) * u[1]),
+                      pack2(silu_fast(g[2]) * u[2], silu_fast(g[3]) * u[3])};
           } else {
             const f32x4 y = acc[mi][ni];
+            const float rs = t.rs[mi];
             outv[mi * NPM + ni] =
-                u32x2{pack_bf16x2(y[0] * rs, y[1] * rs), pack_bf16x2(y[2] * rs, y[3] * rs)};
+                u32x2{pack2(y[0] * rs, y[1] * rs), pack2(y[2] * rs, y[3] * rs)};
           }
         }
       }
     }
-    raw_barrier();   // every wave is done reading the ring
+    // every wave is done reading the ring, and the mail is there
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    raw_barrier();
     const MxTile<R> done = t;
-    tile += G;
-    if (tile < total) {
-      mx_ring_setup<MODE, AF4, R, BM>(args, tiles_l, tile, t);
+    next = read_mail(slot);
+    const bool more = next.pi >= 0;
+    if (more) {
+      mx_ring_setup<MODE, AF4, R, BM>(args, next, t);
       if (wvs < R::NI) mx_ring_prologue<MODE, AF4, R, BM>(t, ring, wvs);
     }
+    if (more) ticket = fetch();
+    // the copies stay before the stores: the waits count on their order
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
     mx_ring_store<MODE, AF4, R, BM>(args.p[done.pi], done, outv, ring + (STAGES - 1) * R::STAGE_CH);
-    if (tile >= total) break;
+    if (!more) break;
+    stores = true;
   }
 }
+
+constexpr int kMxClasses = 3;
 
 // One grouped GEMM over three classes of segments: up to 64 rows (64-row tiles,
 // bound by reading their experts' weights), up to 255 (128-row tiles; with
 // bf16 activations all longer ones too) and, with FP4 activations, 256 and
-// more (256-row tiles, bound by the matrix units).  Every workgroup takes its
-// share of each class, half of them in the opposite order, so that the
-// classes that wait for memory and those that compute run side by side.
+// more (256-row tiles, bound by the matrix units).  Every workgroup works on
+// each class, half of them in the opposite order, so that the classes that
+// wait for memory and those that compute run side by side.
 template <int MODE, bool AF4, int STAGES, bool BIG>
 __global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
   // (the ring and the tile table are the only LDS objects, as in gemm.hip's
   // ring kernel)
   __shared__ __attribute__((aligned(1024))) u32x4 ring[mx_ring_lds<AF4, STAGES, BIG>()];
   extern __shared__ int tiles_l[];
-  const int G = gridDim.x, logical = xcd_logical(blockIdx.x, G);
-  // (the classes' last, partial rounds start at different workgroups)
-  const int second = (logical + G / 3) % G, third = (logical + 2 * (G / 3)) % G;
+  const int odd = xcd_logical(blockIdx.x, gridDim.x) & 1;
+  int32_t* queue = args.queue + blockIdx.x % 8;
   constexpr int n = BIG ? 3 : 2;
   for (int i = 0; i < n; ++i) {
-    switch (logical & 1 ? i : n - 1 - i) {
+    switch (odd ? i : n - 1 - i) {
       case 0:
-        mx_ring_class<MODE, AF4, 64, STAGES, 2>(args, ring, tiles_l, 1, kMxSmall + 1, logical);
+        mx_ring_class<MODE, AF4, 64, STAGES, 2>(args, ring, tiles_l, 1, kMxSmall + 1, queue);
         break;
       case 1:
         mx_ring_class<MODE, AF4, 128, STAGES, 2>(args, ring, tiles_l, kMxSmall + 1,
-                                                 BIG ? kMxBig : kAll, second);
+                                                 BIG ? kMxBig : kAll, queue + 8);
         break;
       default:
         if constexpr (BIG)
-          mx_ring_class<MODE, AF4, 256, 2, 4>(args, ring, tiles_l, kMxBig, kAll, third);
+          mx_ring_class<MODE, AF4, 256, 2, 4>(args, ring, tiles_l, kMxBig, kAll, queue + 16);
         break;
     }
   }
+}
+
+// Clears the queues of one call's two GEMMs.
+__global__ __launch_bounds__(64) void mx_queue_kernel(int32_t* queue) {
+  if (threadIdx.x < 2 * kMxClasses * 8) queue[threadIdx.x] = 0;
 }
 
 MxArgs cover(MxArgs g, int bm, int ncols, int min_len, int max_len) {
@@ -951,7 +1070,7 @@ void launch_stream_ks(const MxArgs& g, hipStream_t s) {
 // ring.
 template <int MODE, bool AF4, int STAGES, bool BIG>
 bool launch_ring(const MxArgs& g, hipStream_t s) {
-  const size_t dyn = (size_t)(g.n_seg_total + 1) * sizeof(int);
+  const size_t dyn = (size_t)(g.n_seg_total + 1 + 12) * sizeof(int);   // the table and the mail
   if ((size_t)mx_ring_lds<AF4, STAGES, BIG>() * 16 + dyn + 64 > kMaxLdsBytes) return false;
   auto k = mx_ring_kernel<MODE, AF4, STAGES, BIG>;
   k<<<persistent_grid(k, dyn, 1, 512), 512, dyn, s>>>(g);
@@ -959,8 +1078,8 @@ bool launch_ring(const MxArgs& g, hipStream_t s) {
 }
 
 // (the smallest rings fit beside the longest table: routed and shared segments)
-static_assert(mx_ring_lds<true, 2, false>() * 16 + (kMaxSegments + 2) * 4 + 64 <= kMaxLdsBytes &&
-                  mx_ring_lds<false, 2, false>() * 16 + (kMaxSegments + 2) * 4 + 64 <= kMaxLdsBytes,
+static_assert(mx_ring_lds<true, 2, false>() * 16 + (kMaxSegments + 2 + 12) * 4 + 64 <= kMaxLdsBytes &&
+                  mx_ring_lds<false, 2, false>() * 16 + (kMaxSegments + 2 + 12) * 4 + 64 <= kMaxLdsBytes,
               "every launch has a ring");
 
 template <int MODE, bool AF4>
@@ -1034,6 +1153,11 @@ void launch_grouped_ffn_mx(const moe_config& c, const FfnProblem* probs, int n_p
     longest = probs[p].max_seg_rows > longest ? probs[p].max_seg_rows : longest;
   }
   const bool few = uses_decode_tiles(rows, nst);
+  if (!few) {
+    g1.queue = probs[0].queue;
+    g2.queue = probs[0].queue + kMxClasses * 8;
+    mx_queue_kernel<<<1, 64, 0, s>>>(probs[0].queue);
+  }
   if (probs[0].mx_acts) {
     launch_gemm<0, true>(g1, few, longest, s);
     launch_gemm<1, true>(g2, few, longest, s);

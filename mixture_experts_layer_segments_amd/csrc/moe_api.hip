@@ -52,6 +52,7 @@ Layout make_layout(const moe_config& c) {
     const bool dec = c.act_dtype == MOE_DT_BF16 && uses_decode_tiles(rows, segs);
     L.a_deq = take(dec ? std::max((size_t)c.T, R) * c.H * 2 : 0);
   }
+  L.queue = take(256);
   L.g_end = o;
   L.y_perm = take(R * c.H * eb);
   L.shared_y = take(c.shared_I > 0 ? (size_t)c.T * c.H * eb : 0);
@@ -235,9 +236,10 @@ moe_status grouped_ffn(const moe_config* cfg, const void* x_perm, const void* x_
   p.a_e8 = (const uint8_t*)x_perm_scale;
   p.h_e8 = (uint8_t*)(ws + L.h_s);   // (as many bytes as the 1 x 128 fp32 scales)
   p.h_q = (uint8_t*)(ws + L.h_q);
+  p.queue = (int32_t*)(ws + L.queue);
   p.h_scale = (float*)(ws + L.h_s);
   p.a_deq = ws + L.a_deq;
-  p.a_deq_bytes = L.g_end - L.a_deq;
+  p.a_deq_bytes = L.queue - L.a_deq;
   launch_grouped_ffn(*cfg, &p, 1, (hipStream_t)stream);
   return launch_status();
 }
@@ -307,9 +309,10 @@ moe_status layer_forward(const moe_config* cfg, const float* logits, const void*
   p[0].a_fp8 = w.acts_fp8;
   p[0].a_scale = xs;
   p[0].h_q = (uint8_t*)(ws + L.h_q);
+  p[0].queue = (int32_t*)(ws + L.queue);
   p[0].h_scale = (float*)(ws + L.h_s);
   p[0].a_deq = ws + L.a_deq;
-  p[0].a_deq_bytes = L.g_end - L.a_deq;
+  p[0].a_deq_bytes = L.queue - L.a_deq;
   p[0].a_rows = r2t;
   p[0].mx = w.mx;
   p[0].mx_acts = w.acts_mx;
@@ -341,7 +344,7 @@ moe_status layer_forward(const moe_config* cfg, const float* logits, const void*
     p[1].h_q = (uint8_t*)(ws + L.shared_hq);
     p[1].h_scale = (float*)(ws + L.shared_hs);
     p[1].a_deq = ws + L.a_deq;
-    p[1].a_deq_bytes = L.g_end - L.a_deq;
+    p[1].a_deq_bytes = L.queue - L.a_deq;
     p[1].mx = sw.mx;
     p[1].mx_acts = sw.acts_mx;
     p[1].w13_e8 = sw.w13_e8;

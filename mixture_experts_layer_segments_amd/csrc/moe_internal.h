@@ -92,8 +92,9 @@ struct Layout {
   size_t cnt_bin, blk_off, seg_of_bin, p_end;                 // region P
   size_t h, shared_h,                                         // region G
       h_q, h_s, shared_hq, shared_hs,                         //   (FP8 activations: h quantized)
-      a_deq, g_end;                                           //   (FP8 activations, decode tiles:
+      a_deq,                                                  //   (FP8 activations, decode tiles:
                                                               //    the activations in bf16)
+      queue, g_end;                                           //   (MXFP4: tile queues)
   size_t y_perm, shared_y, seg_offsets, seg_expert,           // region L
       assign_to_row, row_to_token, row_w,
       x_q, x_s, l_end;                                        //   (FP8 activations: x quantized)
@@ -159,6 +160,7 @@ struct FfnProblem {
   const uint8_t* w2_e8;   // [n_w, K1, Iw/32]
   const uint8_t* a_e8;
   uint8_t* h_e8;
+  int32_t* queue;         // tile queues of the call's two GEMMs (256 bytes; the first problem's)
 };
 void launch_grouped_ffn(const moe_config& c, const FfnProblem* probs, int n_probs,
                         hipStream_t s);
