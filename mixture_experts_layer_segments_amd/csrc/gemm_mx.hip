@@ -379,20 +379,33 @@ void mx_stream_kernel(MxArgs args) {
 // completion as in gemm.hip's ring: waves 0-3 issue, explicit vmcnt waits, a
 // plain barrier a stage).
 //
-// A stage holds, per row, 128 bytes of codes (256 elements) with FP4
-// activations, and 256 bytes of bf16 / 64 bytes of codes (128 elements) with
-// bf16 ones, in 16-byte chunks XOR-swizzled by row.  (Stages half as deep and
-// twice as many were 15-20% slower: a 64-byte piece costs a request as a whole
-// line does.)  The rows' E8M0 bytes come 16 at a time, those of 512 elements,
-// into two slots of their own behind the ring: a 4- or 8-byte piece per stage
-// cost as many requests as the codes (measured: 10-20% of a launch).
+// A stage holds, per row, 128 bytes of codes (256 elements), in 64-row and in
+// FP4 tiles; longer bf16 tiles, where the activations take most of the LDS,
+// 256 bytes of bf16 and 64 bytes of codes (128 elements); in 16-byte chunks
+// XOR-swizzled by row.  A 64-byte piece costs a request as a whole line does:
+// FP4 stages half as deep and twice as many were 15-20% slower, 64-row bf16
+// tiles 12% (458 against 409 us for 128 segments of 64 rows, H 4096, I 1536).
+// The rows' E8M0 bytes come 16 at a time, those of 512 elements, into two
+// slots of their own behind the ring: a 4- or 8-byte piece per stage cost as
+// many requests as the codes (10-20% of a launch).
 //
 // FP4 activations: two 16x16x128 FP4 matrix steps a stage.  Lane (r, q)
 // supplies chunk 4 s + q of row r (32 elements, one scale block) and byte
 // 4 s + q of the stage's scales.
-// bf16 activations: lane (r, q) reads chunk q of weight row r, 32 codes and
-// one scale, and feeds them to four 16x16x32 steps, 8 at a time, against
-// chunk 4 q + m of the activation row in step m.
+// bf16 activations: lane (r, q) reads chunk 4 s + q of weight row r, 32 codes
+// and one scale, and feeds them to four 16x16x32 steps, 8 at a time, against
+// chunk 16 s + 4 q + m of the activation row in step m.  On 64-row tiles the
+// eight waves take 32 weight rows each and all the activation rows, so that
+// no code is converted twice (4-9% faster than two rows of waves).
+//
+// What bounds them, measured with a part left out, 32 segments of 2048 rows, H
+// 4096, I 1536, FP4 activations (470 + 305 us, 3.3 PFLOP/s): copies and
+// stores without the products 365 + 243 us, products and stores without the
+// copies 380 + 214, all but the stores 411 + 218.  The copies move 64 KiB a
+// stage in about 3500 cycles of a compute unit whatever the rows' stride and
+// whether the L2 holds the lines already, the products take 2050.  With bf16
+// activations long segments run at 1.2 PFLOP/s, near a large bf16 library
+// product's 1.29.
 //
 // Tiles are chained: when a tile's K loop is done, the copies of the next
 // tile's first stages are issued before the output is formed, which is staged
@@ -400,8 +413,8 @@ void mx_stream_kernel(MxArgs args) {
 template <bool AF4, int BM, int STAGES_, int WM_>
 struct MxRing {
   static constexpr int WAVES_M = WM_, BN = 256, NTHR = 512, NI = 4, STAGES = STAGES_;
-  static constexpr int BK = AF4 ? 256 : 128;              // elements of a stage
-  static constexpr int KCA = AF4 ? 8 : 16, KCB = AF4 ? 8 : 4;   // chunks per row
+  static constexpr int BK = AF4 || BM == 64 ? 256 : 128;  // elements of a stage
+  static constexpr int KCA = AF4 ? BK / 32 : BK / 8, KCB = BK / 32;   // chunks per row
   static constexpr int RPA = 64 / KCA, RPB = 64 / KCB;    // rows per 1 KiB copy
   static constexpr int A_CH = BM * KCA, B_CH = BN * KCB, STAGE_CH = A_CH + B_CH;
   static constexpr int SG = 512 / BK;                     // stages of a scale group
@@ -687,41 +700,46 @@ __device__ __forceinline__ void mx_ring_mma(const u32x4* ring, int kt, int wm, i
       __builtin_amdgcn_sched_barrier(0);
     }
   } else {
-    const uint32_t* sb1 = reinterpret_cast<const uint32_t*>(sc + brow) + (kt & 3);
-    u32x4 bc[TN], a[2][NM];
-    uint32_t bs[TN];
-    auto load_a = [&](int m, int mi) {
-      a[m & 1][mi] = As[mi * AF * R::KCA + ((4 * q + m) ^ swz<R::KCA>(r))];
-    };
+    const uint32_t* sb1 =
+        reinterpret_cast<const uint32_t*>(sc + brow) + kt % R::SG * (R::BK / 128);
+    // 128 elements of K at a time
 #pragma unroll
-    for (int ni = 0; ni < TN; ++ni) {
-      bc[ni] = Bs[b_at(ni) * R::KCB + (q ^ swz<R::KCB>(r))];
-      bs[ni] = sb1[b_at(ni) * 4];
-    }
+    for (int s = 0; s < NS; ++s) {
+      u32x4 bc[TN], a[2][NM];
+      uint32_t bs[TN];
+      auto load_a = [&](int m, int mi) {
+        a[m & 1][mi] = As[mi * AF * R::KCA + ((16 * s + 4 * q + m) ^ swz<R::KCA>(r))];
+      };
 #pragma unroll
-    for (int mi = 0; mi < NM; ++mi) load_a(0, mi);
-    float bf[TN];
+      for (int ni = 0; ni < TN; ++ni) {
+        bc[ni] = Bs[b_at(ni) * R::KCB + ((4 * s + q) ^ swz<R::KCB>(r))];
+        bs[ni] = sb1[b_at(ni) * 4 + s];
+      }
 #pragma unroll
-    for (int ni = 0; ni < TN; ++ni) bf[ni] = e8m0_float((bs[ni] >> (8 * q)) & 0xffu);
-    u32x4 b = e2m1x8_to_bf16(bc[0][0], bf[0]);
+      for (int mi = 0; mi < NM; ++mi) load_a(0, mi);
+      float bf[TN];
 #pragma unroll
-    for (int x = 0; x < 4 * TN; ++x) {
-      const int m = x / TN, ni = x % TN;
-      if (m < 3) {
+      for (int ni = 0; ni < TN; ++ni) bf[ni] = e8m0_float((bs[ni] >> (8 * q)) & 0xffu);
+      u32x4 b = e2m1x8_to_bf16(bc[0][0], bf[0]);
+#pragma unroll
+      for (int x = 0; x < 4 * TN; ++x) {
+        const int m = x / TN, ni = x % TN;
+        if (m < 3) {
+#pragma unroll
+          for (int mi = 0; mi < NM; ++mi)
+            if (mi * TN / NM == ni) load_a(m + 1, mi);
+        }
+        u32x4 nb = b;
+        if (x + 1 < 4 * TN)
+          nb = e2m1x8_to_bf16(bc[(x + 1) % TN][(x + 1) / TN], bf[(x + 1) % TN]);
 #pragma unroll
         for (int mi = 0; mi < NM; ++mi)
-          if (mi * TN / NM == ni) load_a(m + 1, mi);
+          acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a[m & 1][mi]),
+              acc[mi][ni], 0, 0, 0);
+        b = nb;
+        __builtin_amdgcn_sched_barrier(0);
       }
-      u32x4 nb = b;
-      if (x + 1 < 4 * TN)
-        nb = e2m1x8_to_bf16(bc[(x + 1) % TN][(x + 1) / TN], bf[(x + 1) % TN]);
-#pragma unroll
-      for (int mi = 0; mi < NM; ++mi)
-        acc[mi][ni] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-            __builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, a[m & 1][mi]), acc[mi][ni],
-            0, 0, 0);
-      b = nb;
-      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
@@ -755,9 +773,9 @@ __device__ __forceinline__ void mx_ring_kloop(const MxTile<R>& t, u32x4* ring, i
   const int full = K / R::BK;
   for (int kt = 0; kt < full; ++kt) {
     enter(kt);
-    if constexpr (NM > 0) mx_ring_mma<MODE, AF4, R, NM, AF4 ? 2 : 1>(ring, kt, wm, wn, lane, acc);
+    if constexpr (NM > 0) mx_ring_mma<MODE, AF4, R, NM, R::BK / 128>(ring, kt, wm, wn, lane, acc);
   }
-  if (AF4 && full < KT) {
+  if (R::BK == 256 && full < KT) {
     enter(full);
     if constexpr (NM > 0) mx_ring_mma<MODE, AF4, R, NM, 1>(ring, full, wm, wn, lane, acc);
   }
@@ -875,7 +893,7 @@ constexpr int kMxSmall = 64, kMxBig = 256;
 // 16-byte chunks of LDS that the classes of a launch need.
 template <bool AF4, int STAGES, bool BIG>
 constexpr int mx_ring_lds() {
-  constexpr int a = MxRing<AF4, 64, STAGES, 2>::LDS_CH, b = MxRing<AF4, 128, STAGES, 2>::LDS_CH,
+  constexpr int a = MxRing<AF4, 64, AF4 ? STAGES : 2, AF4 ? 2 : 1>::LDS_CH, b = MxRing<AF4, 128, STAGES, 2>::LDS_CH,
                 c = BIG ? MxRing<AF4, 256, 2, 4>::LDS_CH : 0;
   return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
@@ -993,7 +1011,8 @@ __device__ __forceinline__ void mx_ring_class(const MxArgs& args, u32x4* ring, i
 constexpr int kMxClasses = 3;
 
 // One grouped GEMM over three classes of segments: up to 64 rows (64-row tiles,
-// bound by reading their experts' weights), up to 255 (128-row tiles; with
+// bound by reading their experts' weights: 5.3 TB/s
+// of codes with FP4 activations, 3.2 - 4.4 with bf16 ones), up to 255 (128-row tiles; with
 // bf16 activations all longer ones too) and, with FP4 activations, 256 and
 // more (256-row tiles, bound by the matrix units).  Every workgroup works on
 // each class, half of them in the opposite order, so that the classes that
@@ -1010,7 +1029,7 @@ __global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
   for (int i = 0; i < n; ++i) {
     switch (odd ? i : n - 1 - i) {
       case 0:
-        mx_ring_class<MODE, AF4, 64, STAGES, 2>(args, ring, tiles_l, 1, kMxSmall + 1, queue);
+        mx_ring_class<MODE, AF4, 64, AF4 ? STAGES : 2, AF4 ? 2 : 1>(args, ring, tiles_l, 1, kMxSmall + 1, queue);
         break;
       case 1:
         mx_ring_class<MODE, AF4, 128, STAGES, 2>(args, ring, tiles_l, kMxSmall + 1,
