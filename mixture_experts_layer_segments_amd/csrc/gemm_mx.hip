@@ -1011,12 +1011,14 @@ __device__ __forceinline__ void mx_ring_class(const MxArgs& args, u32x4* ring, i
 constexpr int kMxClasses = 3;
 
 // One grouped GEMM over three classes of segments: up to 64 rows (64-row tiles,
-// bound by reading their experts' weights: 5.3 TB/s
-// of codes with FP4 activations, 3.2 - 4.4 with bf16 ones), up to 255 (128-row tiles; with
-// bf16 activations all longer ones too) and, with FP4 activations, 256 and
-// more (256-row tiles, bound by the matrix units).  Every workgroup works on
-// each class, half of them in the opposite order, so that the classes that
-// wait for memory and those that compute run side by side.
+// bound by reading their experts' weights: 5.3 TB/s of codes with FP4
+// activations, 3.2 to 4.5 with bf16 ones, whose codes are converted), up to 255
+// (128-row tiles; with bf16 activations all longer ones too) and, with FP4
+// activations, 256 and more (256-row tiles, bound by the copies and the
+// matrix units alike).  Every workgroup works on each class, half of them in
+// the opposite order, so that the classes that wait for memory and those that
+// compute run side by side (4096 tokens, 256 experts, FP4 activations: 1597
+// us, all from the largest class down 1620, from the smallest up 1652).
 template <int MODE, bool AF4, int STAGES, bool BIG>
 __global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
   // (the ring and the tile table are the only LDS objects, as in gemm.hip's
@@ -1064,10 +1066,12 @@ void launch_stream(const MxArgs& g, int min_len, int max_len, hipStream_t s) {
       cover(g, 16, 16 * TN / (MODE == 0 ? 2 : 1), min_len, max_len));
 }
 
-// Waves per tile: enough of them to leave each at most 8 stages of K (K = 8192:
-// 4 waves 191 us, 2 waves 206, 1 wave 202; K = 2048: 1 wave 102 us, 2 waves
-// 112, 4 waves 186), and more where the launch has fewer tiles than the
-// chip takes waves.
+// Waves per tile: enough of them to leave each at most 8 stages of K, and more
+// where the launch has fewer tiles than the chip takes waves.  us with 4 / 2 /
+// 1 waves, 64 tokens, 64 experts: K = 8192 192 / 204 / 205 (bf16 activations),
+// 171 / 166 / 186 (FP4); K = 2048 192 / 116 / 104 and 139 / 89 / 82.  One
+// token, 8 experts, bf16: K = 7168 28.4 / 27.7 / 41.4, K = 2048 29.5 / 19.1 /
+// 16.8.
 template <int MODE, bool AF4, int TN, int WPE>
 void launch_stream_ks(const MxArgs& g, hipStream_t s) {
   const int64_t ncols = 16 * TN / (MODE == 0 ? 2 : 1);
@@ -1105,8 +1109,8 @@ template <int MODE, bool AF4>
 void launch_gemm(const MxArgs& g, bool few_rows, int longest, hipStream_t s) {
   if (few_rows) {
     // GEMM 1 with FP4 activations takes 32 gate and 32 up rows, so that a tile
-    // holds whole 1 x 32 blocks of h; the others 32 weight rows (64 measured
-    // 2-4% slower)
+    // holds whole 1 x 32 blocks of h; the others 32 weight rows (64, us: bf16
+    // activations 200 + 199 against 192 + 104, FP4 GEMM 2 85.6 against 84.2)
     if constexpr (AF4) launch_stream_ks<MODE, AF4, MODE == 0 ? 4 : 2, MODE == 0 ? 2 : 3>(g, s);
     else launch_stream_ks<MODE, AF4, 2, 2>(g, s);
     return;
