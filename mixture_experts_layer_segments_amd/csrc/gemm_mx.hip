@@ -1122,6 +1122,34 @@ void launch_gemm(const MxArgs& g, bool few_rows, int longest, hipStream_t s) {
   if (!launch_ring<MODE, AF4, 3, false>(g, s)) launch_ring<MODE, AF4, 2, false>(g, s);
 }
 
+// Streaming tiles for calls of few rows a segment, ring tiles for the others.
+// The ring reads weights as fast from four rows on, if its tiles (segments by
+// 128 columns of h) are several to a compute unit; with fewer the streaming
+// tiles, 4 to 8 times as many, fill the chip better.  us streaming / ring, 2
+// experts a token of mild skew, H x I = 4096 x 1536:
+//   rows a segment        2          4          8          16
+//   bf16, 8 experts    33 / 48    34 / 49    39 / 49     53 / 51
+//        32 experts    70 / 87    79 / 88   111 / 89    149 / 90
+//       256 experts   427 / 418  547 / 496  694 / 514  1012 / 558
+//   FP4,  8 experts    32 / 39    34 / 40    35 / 40     42 / 42
+//        32 experts    68 / 70    70 / 72    80 / 78     90 / 79
+//       256 experts   354 / 338  436 / 404  495 / 418   624 / 444
+// (Segments of very different lengths favour the ring: 256 experts, 4 rows on
+// average and 128 at most, 419 / 289 and 283 / 237.)
+bool takes_streaming_tiles(const FfnProblem* probs, int n_probs) {
+  int64_t rows = 0, segs = 0, tiles = 0;
+  for (int p = 0; p < n_probs; ++p) {
+    const int64_t n = probs[p].n_seg, r = probs[p].rows;
+    rows += r;
+    segs += n;
+    tiles += (n < r ? n : r) * (probs[p].Iw / 128);
+  }
+  const int64_t cus = device_cu_count();
+  if (rows < 4 * segs) return true;
+  if (rows <= 8 * segs) return probs[0].mx_acts ? tiles < 3 * cus : tiles <= cus;
+  return rows <= 16 * segs && 3 * tiles <= (probs[0].mx_acts ? 3 : 1) * cus;
+}
+
 }  // namespace
 
 void launch_grouped_ffn_mx(const moe_config& c, const FfnProblem* probs, int n_probs,
@@ -1169,13 +1197,10 @@ void launch_grouped_ffn_mx(const moe_config& c, const FfnProblem* probs, int n_p
   }
   g1.n_probs = g2.n_probs = n_probs;
   g1.n_seg_total = g2.n_seg_total = nst;
-  int64_t rows = 0;
   int longest = 0;
-  for (int p = 0; p < n_probs; ++p) {
-    rows += probs[p].rows;
+  for (int p = 0; p < n_probs; ++p)
     longest = probs[p].max_seg_rows > longest ? probs[p].max_seg_rows : longest;
-  }
-  const bool few = uses_decode_tiles(rows, nst);
+  const bool few = takes_streaming_tiles(probs, n_probs);
   if (!few) {
     g1.queue = probs[0].queue;
     g2.queue = probs[0].queue + kMxClasses * 8;

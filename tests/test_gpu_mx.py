@@ -241,18 +241,21 @@ def test_infinite_gates(moe, a4):
 
 
 @pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
-@pytest.mark.parametrize("n,hot,ways", [(1000, 0, 1), (1024, 0, 1), (600, 600, 2), (1024, 1024, 4)])
-def test_many_segments(moe, n, hot, ways, a4):
-    """More segments than the larger rings leave room for: every length class
+@pytest.mark.parametrize("n,hot,ways,most", [
+    (1000, 0, 1, 38), (1024, 0, 1, 38), (600, 600, 2, 38), (1024, 1024, 4, 38),
+    (1000, 0, 1, 10), (300, 0, 1, 12), (300, 0, 1, 28), (90, 0, 1, 28), (1000, 0, 1, 5)])
+def test_many_segments(moe, n, hot, ways, most, a4):
+    """More segments than the larger rings leave room for, and segments of
+    few rows each, on either side of the launch's rules: every length class
     and empty segments among them."""
     rng = np.random.default_rng(n + ways)
     H = I = 128
     S = n + hot * (ways - 1)
-    L = rng.integers(0, 38, S)
+    L = rng.integers(0, most, S)
     L[[1, S // 2, S - 1]] = 300, 257, 130
     cfg = mi.MoEShape("s", T=int(L.sum()) + 3, H=H, E=n, k=1, I=I, n_hot_split=hot,
                       split_ways=ways)
-    assert moe.moe_num_segments(cfg) == S and L.sum() > 16 * S
+    assert moe.moe_num_segments(cfg) == S
     few = mu.Experts(rng, 8, H, I)
 
     class All:
