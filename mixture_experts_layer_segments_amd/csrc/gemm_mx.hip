@@ -1122,32 +1122,31 @@ void launch_gemm(const MxArgs& g, bool few_rows, int longest, hipStream_t s) {
   if (!launch_ring<MODE, AF4, 3, false>(g, s)) launch_ring<MODE, AF4, 2, false>(g, s);
 }
 
-// Streaming tiles for calls of few rows a segment, ring tiles for the others.
-// The ring reads weights as fast from four rows on, if its tiles (segments by
-// 128 columns of h) are several to a compute unit; with fewer the streaming
-// tiles, 4 to 8 times as many, fill the chip better.  us streaming / ring, 2
-// experts a token of mild skew, H x I = 4096 x 1536:
-//   rows a segment        2          4          8          16
-//   bf16, 8 experts    33 / 48    34 / 49    39 / 49     53 / 51
-//        32 experts    70 / 87    79 / 88   111 / 89    149 / 90
-//       256 experts   427 / 418  547 / 496  694 / 514  1012 / 558
-//   FP4,  8 experts    32 / 39    34 / 40    35 / 40     42 / 42
-//        32 experts    68 / 70    70 / 72    80 / 78     90 / 79
-//       256 experts   354 / 338  436 / 404  495 / 418   624 / 444
+// Streaming tiles for calls of few rows a segment or few rows in all, ring
+// tiles for the others.  The ring reads weights as fast from four rows a
+// segment on, if its tiles are several to a compute unit; where they are not,
+// the streaming tiles, 8 times as many and split over K, fill the chip
+// better.  They cross where rows times 128-column tiles of h come to 8 (bf16
+// activations) and 16 (FP4) for each unit.  us streaming / ring, rows a segment:
+//   H x I                              4          16          64          256
+//   4096 x 1536, bf16,   1 expert   22 / 42    28 / 41     27 / 51     71 / 82
+//                        8 experts  34 / 49    50 / 50    110 / 55    398 / 126
+//                      256 experts 547 / 496 1012 / 558
+//                FP4,    1 expert   20 / 36    21 / 36     19 / 39     41 / 60
+//                        8 experts  34 / 40    38 / 40     75 / 48    234 / 64
+//                      256 experts 436 / 404  624 / 444
+//   4096 x 14336, bf16,  1 expert   46 / 113   73 / 113   130 / 125   432 / 254
+//                 FP4,   1 expert   46 / 81    56 / 82     81 / 91    260 / 132
 // (Segments of very different lengths favour the ring: 256 experts, 4 rows on
 // average and 128 at most, 419 / 289 and 283 / 237.)
 bool takes_streaming_tiles(const FfnProblem* probs, int n_probs) {
   int64_t rows = 0, segs = 0, tiles = 0;
   for (int p = 0; p < n_probs; ++p) {
-    const int64_t n = probs[p].n_seg, r = probs[p].rows;
-    rows += r;
-    segs += n;
-    tiles += (n < r ? n : r) * (probs[p].Iw / 128);
+    rows += probs[p].rows;
+    segs += probs[p].n_seg;
+    tiles += (int64_t)probs[p].rows * (probs[p].Iw / 128);
   }
-  const int64_t cus = device_cu_count();
-  if (rows < 4 * segs) return true;
-  if (rows <= 8 * segs) return probs[0].mx_acts ? tiles < 3 * cus : tiles <= cus;
-  return rows <= 16 * segs && 3 * tiles <= (probs[0].mx_acts ? 3 : 1) * cus;
+  return rows < 4 * segs || tiles < (probs[0].mx_acts ? 16 : 8) * (int64_t)device_cu_count();
 }
 
 }  // namespace

@@ -145,9 +145,12 @@ LENS = {
     "edges": [15, 16, 17, 31, 32, 33, 48, 49],
     "mid": [63, 64, 65, 1, 0, 127, 128, 129],
     "long": [300, 0, 255, 256, 257, 1, 513, 40],
+    "longer": [2003, 0, 60, 1500, 90, 64, 700, 3],
 }
 SIZES = {"128x128": (128, 128), "256x384": (256, 384), "640x128": (640, 128),
-         "1152x896": (1152, 896), "2048x512": (2048, 512)}
+         "1152x896": (1152, 896), "2048x512": (2048, 512),
+         # (calls of many rows by columns of h take other tiles)
+         "128x4096": (128, 4096), "384x2048": (384, 2048)}
 
 
 @pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
@@ -176,14 +179,15 @@ def test_grouped_ffn(moe, lens, size, a4):
 
 
 @pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
-def test_nan_and_inf_stay_in_their_rows(moe, a4):
+@pytest.mark.parametrize("I", [256, 2304])
+def test_nan_and_inf_stay_in_their_rows(moe, I, a4):
     """A row with a NaN or an infinity, and an expert with NaN scales, leave
     every other output finite and equal to the run without them; skipped
     segments (another expert id) leave their rows alone."""
     rng = np.random.default_rng(9)
     L = [5, 40, 200, 3]
-    cfg = mi.MoEShape("n", T=sum(L), H=256, E=4, k=1, I=256)
-    ex = mu.Experts(rng, 4, 256, 256)
+    cfg = mi.MoEShape("n", T=sum(L), H=256, E=4, k=1, I=I)
+    ex = mu.Experts(rng, 4, 256, I)
     x = mu.bf16_rows(rng, sum(L), 256)
     clean = _run_ffn(moe, cfg, ex, x, L, [0, 1, 2, -1], None, a4)
     assert (clean[245:] == 7).all()
@@ -203,39 +207,41 @@ def test_nan_and_inf_stay_in_their_rows(moe, a4):
 
 
 @pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
-@pytest.mark.parametrize("rows", [4, 60, 200, 300])
-def test_large_gates(moe, rows, a4):
+@pytest.mark.parametrize("rows,I", [(4, 256), (60, 256), (200, 256), (300, 256), (60, 4608),
+                                    (200, 2048), (300, 2048)])
+def test_large_gates(moe, rows, I, a4):
     """Gates from about -600 to 600: e^-z overflows and underflows."""
     rng = np.random.default_rng(rows)
-    cfg = mi.MoEShape("g", T=2 * rows, H=256, E=2, k=1, I=256)
-    ex = mu.Experts(rng, 2, 256, 256, std=3.0)
+    cfg = mi.MoEShape("g", T=2 * rows, H=256, E=2, k=1, I=I)
+    ex = mu.Experts(rng, 2, 256, I, std=3.0)
     x = mu.bf16_rows(rng, 2 * rows, 256)
     x[0], x[rows, 1:] = 0, 0
     y = _run_ffn(moe, cfg, ex, x, [rows, rows], [1, 0], None, a4)
     for s, e in enumerate((1, 0)):
         sl = slice(s * rows, (s + 1) * rows)
-        gate = x[sl] @ ex.w13[e][:256].T
+        gate = x[sl] @ ex.w13[e][:I].T
         assert gate.min() < -150 and gate.max() > 150
         mu.check_close(y[sl], *mu.expert_tol(x[sl], ex.w13[e], ex.w2[e], a4), f"expert {e}")
 
 
 @pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
-def test_infinite_gates(moe, a4):
+@pytest.mark.parametrize("T", [40, 4100])
+def test_infinite_gates(moe, T, a4):
     """silu(inf) = inf; a gate of -inf has no value (-inf times 0)."""
     rng = np.random.default_rng(2)
-    cfg = mi.MoEShape("g", T=40, H=128, E=1, k=1, I=128)
+    cfg = mi.MoEShape("g", T=T, H=128, E=1, k=1, I=128)
     ex = mu.Experts(rng, 1, 128, 128)
     # hidden unit 0: gate = x_0 * 2^100, up = x_1
     ex.q13[0, [0, 128]], ex.s13[0, [0, 128]] = 0, 127
     ex.q13[0, 0, 0], ex.s13[0, 0, 0] = 2, 227        # code 2 = 1.0 at element 0
     ex.q13[0, 128, 0] = 2 << 4                       # 1.0 at element 1
-    x = mu.bf16_rows(rng, 40, 128)
+    x = mu.bf16_rows(rng, T, 128)
     x[:, 0] = 0.0
-    clean = _run_ffn(moe, cfg, ex, x, [40], [0], None, a4)
+    clean = _run_ffn(moe, cfg, ex, x, [T], [0], None, a4)
     assert np.isfinite(clean).all()
     x[3, :2], x[37, :2] = 2.0 ** 100, 2.0 ** 100
-    got = _run_ffn(moe, cfg, ex, x, [40], [0], None, a4)
-    other = np.setdiff1d(np.arange(40), [3, 37])
+    got = _run_ffn(moe, cfg, ex, x, [T], [0], None, a4)
+    other = np.setdiff1d(np.arange(T), [3, 37])
     np.testing.assert_array_equal(got[other], clean[other])
     assert not np.isfinite(got[[3, 37]]).any(1).all()
 
@@ -277,11 +283,12 @@ def test_many_segments(moe, n, hot, ways, most, a4):
 
 
 @pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
-def test_same_call_twice_is_bit_equal(moe, a4):
+@pytest.mark.parametrize("I", [384, 1536])
+def test_same_call_twice_is_bit_equal(moe, I, a4):
     rng = np.random.default_rng(10)
     L = [70, 300, 0, 2]
-    cfg = mi.MoEShape("n", T=sum(L), H=512, E=4, k=1, I=384)
-    ex = mu.Experts(rng, 4, 512, 384)
+    cfg = mi.MoEShape("n", T=sum(L), H=512, E=4, k=1, I=I)
+    ex = mu.Experts(rng, 4, 512, I)
     x = mu.bf16_rows(rng, sum(L), 512)
     a = _run_ffn(moe, cfg, ex, x, L, [0, 1, 2, 3], None, a4)
     for fill in (0, 255):                    # whatever the workspace holds
@@ -302,6 +309,13 @@ LAYERS = {
                             capacity_factor_permille=1250, seed=65),
     "replicas": mi.MoEShape("l6", T=600, H=256, E=8, k=2, I=128, zipf_s=1.0, n_hot_split=2,
                             split_ways=2, shared_I=256, seed=66),
+    # (the same, with enough work for the other tiles)
+    "wide_groups_shared": mi.MoEShape("l7", T=333, H=384, E=16, k=4, I=512, score="sigmoid",
+                                      n_group=4, topk_group=2, shared_I=128, zipf_s=1.0, seed=67),
+    "wide_replicas": mi.MoEShape("l8", T=600, H=256, E=8, k=2, I=512, zipf_s=1.0, n_hot_split=2,
+                                 split_ways=2, shared_I=256, seed=68),
+    "wide_capacity": mi.MoEShape("l9", T=600, H=256, E=16, k=2, I=512, zipf_s=1.0,
+                                 capacity_factor_permille=1250, seed=69),
 }
 
 
@@ -403,7 +417,8 @@ def test_layer(moe, name, a4):
 
 
 @pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
-@pytest.mark.parametrize("name", ["decode", "groups_shared", "capacity"])
+@pytest.mark.parametrize("name", ["decode", "groups_shared", "capacity", "wide_groups_shared",
+                                  "wide_capacity"])
 def test_layer_graph_replays_on_new_inputs(moe, name, a4):
     """Captured once, replayed on other logits and rows with eager work in
     between: every replay equals the eager call."""
@@ -433,8 +448,9 @@ def test_layer_graph_replays_on_new_inputs(moe, name, a4):
             assert torch.equal(a, b)
 
 
-def test_two_streams_with_their_own_workspaces(moe):
-    cfg = LAYERS["decode"]
+@pytest.mark.parametrize("name", ["decode", "wide_replicas"])
+def test_two_streams_with_their_own_workspaces(moe, name):
+    cfg = LAYERS[name]
     lays = []
     for a4 in (False, True):
         lays.append(_Layer(moe, cfg, a4, *_layer_inputs(cfg)))
