@@ -123,7 +123,7 @@ __device__ __forceinline__ void wait_stages(int later) {
 // row & 15, 2-4% faster than row & 7).
 template <int KCH>
 __device__ __forceinline__ int swz(int row) {
-  if constexpr (KCH >= 16) return row & 15;
+  if constexpr (KCH == 16) return row & 15;
   else if constexpr (KCH == 8) return (row >> 1) & 7;
   else return (row >> 2) & 3;
 }

@@ -410,6 +410,21 @@ void mx_stream_kernel(MxArgs args) {
 // Tiles are chained: when a tile's K loop is done, the copies of the next
 // tile's first stages are issued before the output is formed, which is staged
 // in the one ring slot they leave free.
+// XOR swizzle of the 16-byte chunks of a staged row of KCH chunks (a power of
+// two of at most a 256-byte bank row, or two bank rows).  The 64 lanes of a
+// 16-byte LDS read are served sixteen at a time, lanes 0-3, 12-15 and 20-27,
+// then the other sixteen of 32: of an operand read (row = lane % 16, chunk by
+// lane / 16), two sets of rows for two neighbouring chunks.  Each sixteen hit
+// distinct 16-byte groups of a bank row.  (Swizzles that spread the sixteen
+// rows of one chunk, row & 15 and row / 4 % 4, left a conflict on every read
+// of 256- and 64-byte rows: half of the LDS's cycles, 2% of the time.)
+template <int KCH>
+__device__ __forceinline__ int mx_swz(int row) {
+  if constexpr (KCH >= 16) return (row & 11) | ((row >> 1) & 4);
+  else if constexpr (KCH == 8) return (row >> 1) & 7;
+  else return (row >> 2) & 2;
+}
+
 template <bool AF4, int BM, int STAGES_, int WM_>
 struct MxRing {
   static constexpr int WAVES_M = WM_, BN = 256, NTHR = 512, NI = 4, STAGES = STAGES_;
@@ -536,10 +551,10 @@ __device__ __forceinline__ void mx_ring_setup(const MxArgs& args, const MxPlace&
 #pragma unroll
   for (int i = 0; i < R::A_IT; ++i) {
     const int row = (i * R::NI + wvs) * R::RPA + lane / R::KCA;
-    t.va[i] = a_src(row) * arow_b + ((lane % R::KCA) ^ swz<R::KCA>(row)) * 16;
+    t.va[i] = a_src(row) * arow_b + ((lane % R::KCA) ^ mx_swz<R::KCA>(row)) * 16;
   }
   const int br = wvs * R::RPB + lane / R::KCB;
-  t.vb = (uint32_t)(t.n0 + br) * brow_b + ((lane % R::KCB) ^ swz<R::KCB>(br)) * 16;
+  t.vb = (uint32_t)(t.n0 + br) * brow_b + ((lane % R::KCB) ^ mx_swz<R::KCB>(br)) * 16;
   // scales: a lane a row, 64 rows a copy (a wave past the activation rows
   // repeats the last 64: every wave issues as many copies)
   t.vsa = 0;
@@ -663,10 +678,10 @@ __device__ __forceinline__ void mx_ring_mma(const u32x4* ring, int kt, int wm, i
     int sa[NM], sb[TN];
     u32x4 a[2][NM], b[3];
     auto load_a = [&](int s, int mi) {
-      a[s][mi] = As[mi * AF * R::KCA + ((s * 4 + q) ^ swz<R::KCA>(r))];
+      a[s][mi] = As[mi * AF * R::KCA + ((s * 4 + q) ^ mx_swz<R::KCA>(r))];
     };
     auto load_b = [&](int x) {
-      b[x % 3] = Bs[b_at(x % TN) * R::KCB + (((x / TN) * 4 + q) ^ swz<R::KCB>(r))];
+      b[x % 3] = Bs[b_at(x % TN) * R::KCB + (((x / TN) * 4 + q) ^ mx_swz<R::KCB>(r))];
     };
 #pragma unroll
     for (int mi = 0; mi < NM; ++mi) sa[mi] = scales(sa2 + mi * AF * 2);
@@ -708,11 +723,11 @@ __device__ __forceinline__ void mx_ring_mma(const u32x4* ring, int kt, int wm, i
       u32x4 bc[TN], a[2][NM];
       uint32_t bs[TN];
       auto load_a = [&](int m, int mi) {
-        a[m & 1][mi] = As[mi * AF * R::KCA + ((16 * s + 4 * q + m) ^ swz<R::KCA>(r))];
+        a[m & 1][mi] = As[mi * AF * R::KCA + ((16 * s + 4 * q + m) ^ mx_swz<R::KCA>(r))];
       };
 #pragma unroll
       for (int ni = 0; ni < TN; ++ni) {
-        bc[ni] = Bs[b_at(ni) * R::KCB + ((4 * s + q) ^ swz<R::KCB>(r))];
+        bc[ni] = Bs[b_at(ni) * R::KCB + ((4 * s + q) ^ mx_swz<R::KCB>(r))];
         bs[ni] = sb1[b_at(ni) * 4 + s];
       }
 #pragma unroll
@@ -794,7 +809,7 @@ __device__ __forceinline__ void mx_ring_kloop_live(const MxTile<R>& t, u32x4* ri
 }
 
 // The tile's output through the free ring slot: every wave stages its rows in
-// a part of its own, chunk c of row rr at c ^ (rr % CPR), in PASSES column
+// a part of its own, its chunks swizzled by row, in PASSES column
 // parts where the slot does not hold them all, and whole 16-byte row chunks go
 // out; a chunk past the segment or past N takes an offset beyond the store's
 // range and is dropped.  GEMM 1 with FP4 activations: after a barrier, 16
@@ -810,6 +825,8 @@ __device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R
   static_assert(CPR <= 16 && 64 % CPR == 0 && WM % RPI == 0, "output transpose shape");
   static_assert(8 * WM * CPR <= R::STAGE_CH, "the staged output fits a slot");
   static_assert(!(MODE == 0 && AF4) || PASSES == 1, "h's blocks cross the waves' columns");
+  // (16 rows' pieces of one chunk spread over a bank row of 256 bytes)
+  auto out_swz = [](int rr) { return rr * CPR / 16 % CPR; };
   int lane = threadIdx.x & 63;
   asm volatile("" : "+v"(lane));   // (addresses formed here, not kept through the K loop)
   const int wv = threadIdx.x >> 6;
@@ -824,7 +841,7 @@ __device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R
 #pragma unroll
       for (int ni = 0; ni < NP; ++ni) {
         const int c = ni * 2 + ((lane >> 4) >> 1);
-        reinterpret_cast<u32x2*>(reg + rr * CPR + (c ^ (rr % CPR)))[(lane >> 4) & 1] =
+        reinterpret_cast<u32x2*>(reg + rr * CPR + (c ^ out_swz(rr)))[(lane >> 4) & 1] =
             out[mi * NPM + p * NP + ni];
       }
     }
@@ -845,7 +862,7 @@ __device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R
         const int frag = row / 16, swm = frag % R::WAVES_M;
         const int rr = frag / R::WAVES_M * 16 + row % 16;
         const u32x4 v =
-            slot[(size_t)(swm * R::WAVES_N + swn) * WM * CPR + rr * CPR + (sc ^ (rr % CPR))];
+            slot[(size_t)(swm * R::WAVES_N + swn) * WM * CPR + rr * CPR + (sc ^ out_swz(rr))];
         float f[8];
         uint32_t a = 0;
 #pragma unroll
@@ -876,7 +893,7 @@ __device__ __forceinline__ void mx_ring_store(const MxProblem& P, const MxTile<R
 #pragma unroll
       for (int it = 0; it < WM / RPI; ++it) {
         const int rr = it * RPI + lane / CPR, c = lane % CPR;
-        const u32x4 v = reg[rr * CPR + (c ^ (rr % CPR))];
+        const u32x4 v = reg[rr * CPR + (c ^ out_swz(rr))];
         const int row = t.m0 + (rr / 16 * R::WAVES_M + wm) * 16 + rr % 16, col = col0 + c * 8;
         const uint32_t off = (row < t.len && col < N)
                                  ? ((uint32_t)row * (uint32_t)N + (uint32_t)col) * 2u
