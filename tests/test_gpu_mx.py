@@ -470,3 +470,67 @@ def test_two_streams_with_their_own_workspaces(moe, name):
     for lay, r in zip(lays, ref):
         for a, b in zip(lay.results(), r):
             assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["decode", "wide_replicas"])
+def test_two_graphs_share_a_workspace(moe, name):
+    """Captured on one workspace and replayed in turn, eager calls on it in
+    between: every replay equals the eager call."""
+    cfg = LAYERS[name]
+    lays = [_Layer(moe, cfg, a4, *_layer_inputs(cfg)) for a4 in (False, True)]
+    lays[1].ws = lays[0].ws
+    ref = []
+    for lay in lays:
+        lay()
+        torch.cuda.synchronize()
+        ref.append(lay.results())
+    graphs = []
+    for lay in lays:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            lay()
+        graphs.append(g)
+    for i in range(6):
+        lay, g, r = lays[i % 2], graphs[i % 2], ref[i % 2]
+        lay.out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(lay.results(), r):
+            assert torch.equal(a, b)
+        lays[(i // 2) % 2]()
+
+
+@pytest.mark.parametrize("a4", [False, True], ids=["w4", "w4a4"])
+@pytest.mark.parametrize("L", [[5, 3], [4100, 70]], ids=["few", "many"])
+def test_weights_beyond_4_gib(moe, L, a4):
+    """Experts on either side of the 32-bit byte offsets of the codes."""
+    E, H, I = 1024, 2048, 4096
+    g = torch.Generator(device=gu.dev()).manual_seed(6)
+
+    def codes(rows, cols):
+        q = torch.randint(0, 256, (E, rows, cols // 2), dtype=torch.uint8, device=gu.dev(),
+                          generator=g)
+        return q, torch.randint(117, 121, (E, rows, cols // 32), dtype=torch.uint8,
+                                device=gu.dev(), generator=g)
+    w = (*codes(2 * I, H), *codes(H, I))
+    n = sum(L)
+    rng = np.random.default_rng(n)
+    cfg = mi.MoEShape("b", T=n, H=H, E=E, k=1, I=I)
+    assert w[0].numel() > 2 ** 33 - 1 and (n < 4 * E) == (L[0] == 5)
+
+    class Dev:
+        def device(self):
+            return w
+    lens = np.zeros(E, np.int64)
+    lens[[400, 900]] = L
+    expert = np.arange(E)
+    expert[[400, 900]] = 1023, 513
+    x = mu.bf16_rows(rng, n, H)
+    y = _run_ffn(moe, cfg, Dev(), x, lens, expert, None, a4)
+    r0 = 0
+    for rows, e in zip(L, (1023, 513)):
+        q13, s13, q2, s2 = (t[e].cpu().numpy() for t in w)
+        w13, w2 = (omx.dequantize_rows(omx.unpack(q), s) for q, s in ((q13, s13), (q2, s2)))
+        pick = np.unique(np.r_[r0:r0 + min(rows, 8), max(r0, r0 + rows - 8):r0 + rows])
+        mu.check_close(y[pick], *mu.expert_tol(x[pick], w13, w2, a4), f"expert {e}")
+        r0 += rows
