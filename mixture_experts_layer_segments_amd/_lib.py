@@ -164,13 +164,15 @@ def _nbytes(t) -> int:
     return t.numel() * t.element_size()
 
 
+# (a Stream object is 2.5 us of a small call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
-        # (a Stream object is 2.5 us of a small call)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None:
+        if _raw_stream is None:
             return torch.cuda.current_stream().cuda_stream
-        return raw(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -289,7 +291,7 @@ def _args(*specs):
     """Addresses of (name, tensor, dtype, numel): each of that type, at least
     that many elements, contiguous and on the current device (addresses and
     None pass as they are)."""
-    addresses, placed, last = [], [], None
+    addresses, placed, last = [], (), None
     for name, t, dtype, numel in specs:
         if t is None or type(t) is int:
             addresses.append(t)
@@ -300,15 +302,16 @@ def _args(*specs):
             raise ValueError(f"{name} must hold {numel} elements, not {t.numel()}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        if t.get_device() != last:   # (one check for a run of one device's)
-            last = t.get_device()
-            placed.append((name, t.device))
+        device = t.get_device()   # -1: not a GPU's
+        if device != last:        # (one check for a run of one device's)
+            last = device
+            placed += ((name, device),)
         addresses.append(t.data_ptr())
     for name, device in placed:
-        if device.type != "cuda":
-            raise ValueError(f"{name} must be on the GPU, not on {device}")
-        if device.index != torch.cuda.current_device():
-            raise ValueError(f"{name} is on {device}, the current device is "
+        if device < 0:
+            raise ValueError(f"{name} must be on the GPU")
+        if device != torch.cuda.current_device():
+            raise ValueError(f"{name} is on cuda:{device}, the current device is "
                              f"cuda:{torch.cuda.current_device()}")
     return addresses
 
