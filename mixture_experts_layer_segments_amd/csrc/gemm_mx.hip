@@ -918,7 +918,10 @@ constexpr int mx_ring_lds() {
 // Every tile of one class: the segments of [min_len, max_len) rows on tiles of
 // BM rows, from the class's queue.  The last wave, which issues no copies,
 // fetches a tile's number and looks it up while the tile before is computed,
-// and leaves the place in `mail`.
+// and leaves the place in `mail`.  (Tiles at a fixed stride, FP4 activations:
+// 1712 us against 1600 for 4096 tokens over 256 experts, 1883 against 1774 for
+// 16384 over 128; bf16 ones 1494 / 1479 and 924 / 924.  The order in which
+// tiles are taken changes no result.)
 template <int MODE, bool AF4, int BM, int STAGES, int WAVES_M>
 __device__ __forceinline__ void mx_ring_class(const MxArgs& args, u32x4* ring, int* tiles_l,
                                               int min_len, int max_len, int32_t* queue) {
@@ -1062,7 +1065,8 @@ __global__ __launch_bounds__(512, 1) void mx_ring_kernel(MxArgs args) {
   }
 }
 
-// Clears the queues of one call's two GEMMs.
+// Clears the queues of one call's two GEMMs (1.4 us; a kernel, so that a
+// captured graph holds no memset).
 __global__ __launch_bounds__(64) void mx_queue_kernel(int32_t* queue) {
   if (threadIdx.x < 2 * kMxClasses * 8) queue[threadIdx.x] = 0;
 }
